@@ -349,8 +349,8 @@ def prepare(case, seed):
             # the pool's pages read back as sequences of one page each
             s["k_read"], s["v_read"] = (nv.KVPlane(s[p + "c"], s[p + "s"]) for p in ("k", "v"))
         if op == "commit":
-            s["planes"] = [nv.PagedKVPlane(c, t, s["pages"]) if case["paged"] else nv.KVPlane(c, t)
-                           for c, t in zip(s["codes"], s["scales"])]
+            s["planes"] = nv.KVPlaneList(nv.PagedKVPlane(c, t, s["pages"]) if case["paged"] else nv.KVPlane(c, t)
+                                         for c, t in zip(s["codes"], s["scales"]))
     return s
 
 
