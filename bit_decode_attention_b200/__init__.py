@@ -30,16 +30,21 @@ __all__ = [
     "mxfp4_cache_bytes", "mxfp4_kv_quantize_append",
     "PagedKVPlane", "nvfp4_kv_quantize_append_paged", "nvfp4_decode_attention_paged",
     "nvfp4_prefill_attention", "nvfp4_decode_attention_append", "nvfp4_set_wait_limit",
+    "nvfp4_qk_norm_rope_append", "nvfp4_qk_norm_rope_append_paged", "nvfp4_tree_attention_workspace",
+    "nvfp4_tree_attention", "nvfp4_tree_attention_paged", "nvfp4_verify_drafts",
+    "KVPlaneList", "nvfp4_kv_commit_path", "nvfp4_kv_commit_path_paged",
 ]
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle of torch.cuda.current_stream(), without building a Stream object
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -343,3 +348,193 @@ def nvfp4_decode_attention_noalloc(q: torch.Tensor, k: KVPlane, v: KVPlane, s_te
         _stream(stream))
     _native.check("nvfp4_decode_attention_noalloc", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# a step of tree-drafted decoding
+# ---------------------------------------------------------------------------
+def _target(stream):
+    """(current device, stream handle) of a call."""
+    cur = torch.cuda.current_device()
+    return cur, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(cur)
+
+
+def _need_kind(k, v, kind):
+    if type(k) is not kind or type(v) is not kind:
+        raise TypeError("k and v must be %s" % kind.__name__)
+
+
+def _like_rows(x: torch.Tensor, counts, dtype) -> torch.Tensor:
+    """A dense output like x; with `counts` the rows behind them are not written: zeros."""
+    return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=dtype, device=x.device)
+
+
+def _qk_norm_rope_append(func, kind, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps, rope_table,
+                         interleaved, positions, n_valid, q_out, new_lens, status, stream):
+    _need_kind(k, v, kind)
+    if q_out is None:
+        q_out = _like_rows(x_q, n_valid, x_q.dtype)
+    st = _native.binding().qk_norm_rope_append(
+        *_target(stream), kind is PagedKVPlane, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps,
+        rope_table, interleaved, positions, n_valid, q_out, new_lens, status)
+    if st:
+        _native.check(func, st)
+    return q_out
+
+
+def nvfp4_qk_norm_rope_append(x_q: torch.Tensor, x_k: torch.Tensor, x_v: torch.Tensor, start_pos: torch.Tensor,
+                              s_tensor_k: torch.Tensor, s_tensor_v: torch.Tensor, k: KVPlane, v: KVPlane,
+                              w_q: Optional[torch.Tensor] = None, w_k: Optional[torch.Tensor] = None,
+                              eps: float = 1e-6, rope_table: Optional[torch.Tensor] = None,
+                              interleaved: bool = False, positions: Optional[torch.Tensor] = None,
+                              n_valid: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                              new_lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """RMS norm of each query and key head (eps < 0: none), rotation by the rows
+    of rope_table [P][R] (R/2 cosines, R/2 sines; None: none), K and V quantized
+    into the cache at slots start_pos[b] + i; returns the queries [B][n][H_q][D].
+    x_q, x_k, x_v [B][n][heads][D] may be slices of one packed projection."""
+    return _qk_norm_rope_append("nvfp4_qk_norm_rope_append", KVPlane, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v,
+                                k, v, w_q, w_k, eps, rope_table, interleaved, positions, n_valid, q_out, new_lens,
+                                status, stream)
+
+
+def nvfp4_qk_norm_rope_append_paged(x_q: torch.Tensor, x_k: torch.Tensor, x_v: torch.Tensor, start_pos: torch.Tensor,
+                                    s_tensor_k: torch.Tensor, s_tensor_v: torch.Tensor, k: PagedKVPlane,
+                                    v: PagedKVPlane, w_q: Optional[torch.Tensor] = None,
+                                    w_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                                    rope_table: Optional[torch.Tensor] = None, interleaved: bool = False,
+                                    positions: Optional[torch.Tensor] = None, n_valid: Optional[torch.Tensor] = None,
+                                    q_out: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """nvfp4_qk_norm_rope_append into paged planes that share one block table."""
+    return _qk_norm_rope_append("nvfp4_qk_norm_rope_append_paged", PagedKVPlane, x_q, x_k, x_v, start_pos, s_tensor_k,
+                                s_tensor_v, k, v, w_q, w_k, eps, rope_table, interleaved, positions, n_valid, q_out,
+                                new_lens, status, stream)
+
+
+def nvfp4_tree_attention_workspace(B: int, N: int, H_q: int, H_kv: int, D: int) -> int:
+    return int(_native.lib().nvfp4_tree_attention_workspace(B, N, H_q, H_kv, D))
+
+
+def _tree_attention(func, kind, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree_mask, n_nodes, softmax_scale, out,
+                    out_dtype, workspace, status, stream):
+    _need_kind(k, v, kind)
+    if out is None:
+        out = _like_rows(q, n_nodes, out_dtype)
+    if workspace is None:
+        B, N, H_q, D = q.shape
+        size = nvfp4_tree_attention_workspace(B, N, H_q, k.codes.shape[1], D)
+        if size == 0:
+            raise ValueError("unsupported attention shape")
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    st = _native.binding().tree_attention(
+        *_target(stream), kind is PagedKVPlane, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree_mask, n_nodes,
+        softmax_scale, out, workspace, status)
+    if st:
+        _native.check(func, st)
+    return out
+
+
+def nvfp4_tree_attention(q: torch.Tensor, k: KVPlane, v: KVPlane, s_tensor_k: torch.Tensor, s_tensor_v: torch.Tensor,
+                         start_pos: torch.Tensor, tree_mask: Optional[torch.Tensor] = None,
+                         n_nodes: Optional[torch.Tensor] = None, softmax_scale: float = 0.0,
+                         out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
+                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of a tree's N nodes (K/V appended at start_pos[b] + i) over the
+    cache; q [B][N][H_q][D] bf16 -> [B][N][H_q][D] of out_dtype.  tree_mask int32
+    [N][ceil(N/32)] or [B][N][ceil(N/32)]: bit j of row i lets node i see node j
+    (None: a chain, j <= i)."""
+    return _tree_attention("nvfp4_tree_attention", KVPlane, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree_mask,
+                           n_nodes, softmax_scale, out, out_dtype, workspace, status, stream)
+
+
+def nvfp4_tree_attention_paged(q: torch.Tensor, k: PagedKVPlane, v: PagedKVPlane, s_tensor_k: torch.Tensor,
+                               s_tensor_v: torch.Tensor, start_pos: torch.Tensor,
+                               tree_mask: Optional[torch.Tensor] = None, n_nodes: Optional[torch.Tensor] = None,
+                               softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                               out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
+                               status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """nvfp4_tree_attention over paged planes that share one block table."""
+    return _tree_attention("nvfp4_tree_attention_paged", PagedKVPlane, q, k, v, s_tensor_k, s_tensor_v, start_pos,
+                           tree_mask, n_nodes, softmax_scale, out, out_dtype, workspace, status, stream)
+
+
+def nvfp4_verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], tokens: torch.Tensor,
+                        parents: torch.Tensor, u_accept: torch.Tensor, u_sample: torch.Tensor,
+                        n_nodes: Optional[torch.Tensor] = None, path: Optional[torch.Tensor] = None,
+                        n_accepted: Optional[torch.Tensor] = None, next_token: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, stream=None):
+    """Walk the drafted tree from node 0 by the given random numbers; returns
+    (path int32 [B][N], -1 behind its end; n_accepted int32 [B]; next_token
+    int32 [B]).  target_probs, draft_probs [B][N][V] (row i follows node i;
+    draft_probs None: the drafts were chosen, not drawn), tokens int32 [B][N],
+    parents int32 [N] or [B][N], u_accept [B][N] and u_sample [B] in [0, 1)."""
+    if path is None or n_accepted is None or next_token is None:
+        B, N, _ = target_probs.shape
+        dev = target_probs.device
+        path = torch.full((B, N), -1, dtype=torch.int32, device=dev) if path is None else path
+        n_accepted = torch.zeros(B, dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
+        next_token = torch.full((B,), -1, dtype=torch.int32, device=dev) if next_token is None else next_token
+    st = _native.binding().verify_drafts(*_target(stream), target_probs, draft_probs, tokens, parents, u_accept, u_sample,
+                                         n_nodes, path, n_accepted, next_token, status)
+    if st:
+        _native.check("nvfp4_verify_drafts", st)
+    return path, n_accepted, next_token
+
+
+class KVPlaneList:
+    """The planes of a cache (all layers' K and V: KVPlane, or PagedKVPlane that
+    share one block table), checked and laid out once for nvfp4_kv_commit_path.
+    Holds the planes; a plane whose tensors are replaced needs a new list."""
+
+    def __init__(self, planes):
+        self.planes = list(planes)
+        if not self.planes:
+            raise ValueError("a plane list needs at least one plane")
+        self.kind = type(self.planes[0])
+        if self.kind not in (KVPlane, PagedKVPlane):
+            raise TypeError("planes must be KVPlane or PagedKVPlane")
+        for p in self.planes:
+            _need_kind(self.planes[0], p, self.kind)
+        self.device = self.planes[0].codes.get_device()
+        if self.device < 0:
+            raise ValueError("planes must be CUDA tensors")
+        data, self.B = _native.binding().planes(self.device, self.kind is PagedKVPlane, self.planes)
+        self._structs = ctypes.create_string_buffer(data, len(data))
+        self.address = ctypes.addressof(self._structs)
+
+    def __len__(self):
+        return len(self.planes)
+
+
+def _commit_path(func, kind, planes, start_pos, path, n_accepted, new_lens, status, stream):
+    if not isinstance(planes, KVPlaneList):
+        planes = KVPlaneList(planes)
+    if planes.kind is not kind:
+        raise TypeError("planes must be %s" % kind.__name__)
+    cur, handle = _target(stream)
+    if planes.device != cur:
+        raise ValueError("planes must be on the current CUDA device (%d), got %d" % (cur, planes.device))
+    st = _native.binding().commit_path(cur, handle, kind is PagedKVPlane, planes.address, len(planes.planes), planes.B,
+                                       start_pos, path, n_accepted, new_lens, status)
+    if st:
+        _native.check(func, st)
+
+
+def nvfp4_kv_commit_path(planes, start_pos: torch.Tensor, path: torch.Tensor, n_accepted: torch.Tensor,
+                         new_lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """Keep the accepted path's cache slots: slot start_pos[b] + path[b][j] moves
+    to start_pos[b] + j for j < n_accepted[b], in every plane given (all layers'
+    K and V as a KVPlaneList or a sequence of KVPlane; one launch for 64 planes)."""
+    _commit_path("nvfp4_kv_commit_path", KVPlane, planes, start_pos, path, n_accepted, new_lens, status, stream)
+
+
+def nvfp4_kv_commit_path_paged(planes, start_pos: torch.Tensor, path: torch.Tensor, n_accepted: torch.Tensor,
+                               new_lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """nvfp4_kv_commit_path in paged planes that share one block table."""
+    _commit_path("nvfp4_kv_commit_path_paged", PagedKVPlane, planes, start_pos, path, n_accepted, new_lens, status,
+                 stream)

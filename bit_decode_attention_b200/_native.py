@@ -41,6 +41,14 @@ EXPORTS = (
     "nvfp4_decode_attention_append",
     "nvfp4_set_wait_limit",
     "nvfp4_prefill_attention",
+    "nvfp4_qk_norm_rope_append",
+    "nvfp4_qk_norm_rope_append_paged",
+    "nvfp4_tree_attention_workspace",
+    "nvfp4_tree_attention",
+    "nvfp4_tree_attention_paged",
+    "nvfp4_verify_drafts",
+    "nvfp4_kv_commit_path",
+    "nvfp4_kv_commit_path_paged",
 )
 
 
@@ -130,8 +138,40 @@ def lib():
     L.nvfp4_set_wait_limit.restype = None
     L.nvfp4_prefill_attention.argtypes = [vp, i32, i32, i32, plane_p, plane_p, vp, vp, vp, f32, vp, vp, vp]
     L.nvfp4_prefill_attention.restype = i32
+    for suffix, pp in (("", plane_p), ("_paged", paged_p)):
+        f = getattr(L, "nvfp4_qk_norm_rope_append" + suffix)
+        f.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp, vp, vp,
+                      vp, vp, pp, pp, vp, vp, vp]
+        f.restype = i32
+        f = getattr(L, "nvfp4_tree_attention" + suffix)
+        f.argtypes = [vp, i32, i32, i32, pp, pp, vp, vp, vp, vp, vp, i64, f32, vp, i32, vp, sz, vp, vp]
+        f.restype = i32
+        f = getattr(L, "nvfp4_kv_commit_path" + suffix)
+        f.argtypes = [pp, i32, i32, vp, vp, vp, vp, vp, vp]
+        f.restype = i32
+    L.nvfp4_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32]
+    L.nvfp4_tree_attention_workspace.restype = sz
+    L.nvfp4_verify_drafts.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.nvfp4_verify_drafts.restype = i32
     _lib = L
     return L
+
+
+_binding = None
+
+
+def binding():
+    """The compiled argument marshalling of the tree-step entry points."""
+    global _binding
+    if _binding is None:
+        lib()                                             # loaded first: the module links against it
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built or does not load (%s); run "
+                               "`python -m bit_decode_attention_b200.build`" % e) from e
+        _binding = module
+    return _binding
 
 
 def check(func_name, status):

@@ -431,4 +431,243 @@ nvfp4_status nvfp4_prefill_attention(const void* q, nvfp4_dtype q_dtype, int C, 
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
+
+// ---------------------------------------------------------------------------
+// A step of tree-drafted decoding.  The contiguous and the paged entry points
+// differ in the addressing only.
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+// The shape and addressing that a call's K and V planes share.
+struct CachePair {
+    uint8_t *kc, *ks, *vc, *vs;
+    int B, H_kv, S_max, D;
+    const int32_t* block_table;
+    int page_tokens, max_pages, num_pages;
+};
+
+bool cache_pair(const nvfp4_kv_plane* k, const nvfp4_kv_plane* v, CachePair& c) {
+    if (!plane_ok(k) || !plane_ok(v)) return false;
+    if (k->B != v->B || k->H_kv != v->H_kv || k->S_max != v->S_max || k->D != v->D) return false;
+    c = CachePair{k->codes, k->scales, v->codes, v->scales, k->B, k->H_kv, k->S_max, k->D, nullptr, 0, 0, 0};
+    return true;
+}
+
+bool cache_pair(const nvfp4_kv_paged_plane* k, const nvfp4_kv_paged_plane* v, CachePair& c) {
+    if (!paged_ok(k) || !paged_ok(v)) return false;
+    if (k->block_table != v->block_table || k->B != v->B || k->H_kv != v->H_kv ||
+        k->page_tokens != v->page_tokens || k->max_pages != v->max_pages || k->D != v->D)
+        return false;
+    c = CachePair{k->codes, k->scales, v->codes, v->scales, k->B, k->H_kv, k->max_pages * k->page_tokens, k->D,
+                  k->block_table, k->page_tokens, k->max_pages,
+                  k->num_pages < v->num_pages ? k->num_pages : v->num_pages};
+    return true;
+}
+
+nvfp4_status run_qk_norm_rope_append(const void* x_q, const void* x_k, const void* x_v, nvfp4_dtype dtype, int n_new,
+                                     int H_q, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                     const void* w_q, const void* w_k, float eps, const float* rope_table,
+                                     int rope_positions, int rope_dims, int rope_interleaved,
+                                     const int32_t* d_positions, const int32_t* d_start_pos,
+                                     const int32_t* d_n_valid, int32_t* d_new_lens, const float* d_s_tensor_k,
+                                     const float* d_s_tensor_v, const CachePair& c, void* q_out, int32_t* d_status,
+                                     nvfp4_stream_t stream) {
+    if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
+    if (n_new < 0 || H_q <= 0 || d_s_tensor_k == nullptr || d_s_tensor_v == nullptr || d_start_pos == nullptr)
+        return NVFP4_ERR_INVALID_ARG;
+    if (d_new_lens != nullptr && (d_new_lens == d_start_pos || d_new_lens == d_n_valid)) return NVFP4_ERR_INVALID_ARG;
+    if (!std::isfinite(eps)) return NVFP4_ERR_INVALID_ARG;
+    if (rope_table == nullptr ? rope_dims != 0 : (rope_dims <= 0 || rope_dims > c.D || rope_dims % 16 != 0 ||
+                                                  rope_positions <= 0 || !aligned16(rope_table)))
+        return NVFP4_ERR_INVALID_ARG;
+    const int per16 = dtype == NVFP4_IN_F32 ? 4 : 8;
+    const int64_t dq = (int64_t)H_q * c.D, dk = (int64_t)c.H_kv * c.D;
+    NormRopeLaunch a{};
+    a.sq = q_stride == 0 ? dq : q_stride;
+    a.sk = k_stride == 0 ? dk : k_stride;
+    a.sv = v_stride == 0 ? dk : v_stride;
+    if (a.sq < dq || a.sk < dk || a.sv < dk || a.sq % per16 != 0 || a.sk % per16 != 0 || a.sv % per16 != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (n_new == 0 || c.B == 0) return NVFP4_OK;
+    if (x_q == nullptr || x_k == nullptr || x_v == nullptr || q_out == nullptr || !aligned16(x_q) || !aligned16(x_k) ||
+        !aligned16(x_v) || !aligned16(q_out) || !aligned16(w_q) || !aligned16(w_k))
+        return NVFP4_ERR_INVALID_ARG;
+    // the kernel counts (token, group of four heads) tasks in 31 bits
+    if ((int64_t)c.B * n_new > (int64_t)INT32_MAX / ((H_q + 2 * (int64_t)c.H_kv + 3) / 4 + 1))
+        return NVFP4_ERR_UNSUPPORTED;
+    a.xq = x_q; a.xk = x_k; a.xv = x_v;
+    a.f32 = dtype == NVFP4_IN_F32;
+    a.wq = w_q; a.wk = w_k;
+    a.table = rope_table;
+    a.positions = d_positions; a.start = d_start_pos; a.n_valid = d_n_valid; a.new_lens = d_new_lens;
+    a.st_k = d_s_tensor_k; a.st_v = d_s_tensor_v;
+    a.q_out = q_out;
+    a.kc = c.kc; a.ks = c.ks; a.vc = c.vc; a.vs = c.vs;
+    a.block_table = c.block_table;
+    a.status = d_status;
+    a.B = c.B; a.n = n_new; a.Hq = H_q; a.Hkv = c.H_kv; a.D = c.D; a.S_max = c.S_max;
+    a.R = rope_dims; a.P = rope_positions;
+    a.page_tokens = c.page_tokens; a.max_pages = c.max_pages; a.num_pages = c.num_pages;
+    a.eps = eps;
+    a.interleaved = rope_interleaved != 0;
+    return from_cuda(launch_qk_norm_rope_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status run_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H_q, const CachePair& c,
+                                const float* d_s_tensor_k, const float* d_s_tensor_v, const int32_t* d_start_pos,
+                                const int32_t* d_n_nodes, const int32_t* d_tree_mask, int64_t mask_stride,
+                                float softmax_scale, void* out, nvfp4_dtype out_dtype, void* workspace,
+                                size_t workspace_bytes, int32_t* d_status, nvfp4_stream_t stream) {
+    if (q_dtype != NVFP4_IN_BF16 && q_dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
+    if (out_dtype != NVFP4_IN_BF16 && out_dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
+    if (N < 0 || H_q <= 0 || (H_q % c.H_kv) != 0) return NVFP4_ERR_INVALID_ARG;
+    if (d_s_tensor_k == nullptr || d_s_tensor_v == nullptr || d_start_pos == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (!(std::isfinite(softmax_scale)) || softmax_scale < 0.0f) return NVFP4_ERR_INVALID_ARG;
+    const int64_t words = ((int64_t)N + 31) / 32;
+    if (d_tree_mask != nullptr && mask_stride != 0 && mask_stride < N * words) return NVFP4_ERR_INVALID_ARG;
+    if (q_dtype != NVFP4_IN_BF16 || N > kTreeMaxNodes || H_q / c.H_kv > 128) return NVFP4_ERR_UNSUPPORTED;
+    if (c.B == 0 || N == 0) return NVFP4_OK;
+    if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return NVFP4_ERR_INVALID_ARG;
+    // the kernel numbers a launch's (unit, 128-token tile) pairs in 32 bits
+    const int64_t units = (int64_t)(c.B < kMaxBatchPerLaunch ? c.B : kMaxBatchPerLaunch) * c.H_kv *
+                          (((int64_t)N * (H_q / c.H_kv) + 127) / 128);
+    const int64_t tiles = ((int64_t)c.S_max + 127) / 128;
+    if (units > (int64_t)INT32_MAX / tiles) return NVFP4_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned16(workspace) ||
+        workspace_bytes < tree_attention_workspace(c.B, N, H_q, c.H_kv, c.D))
+        return NVFP4_ERR_WORKSPACE;
+    TreeLaunch a{};
+    a.q = q;
+    a.out_bf16 = out_dtype == NVFP4_IN_BF16;
+    a.B = c.B; a.N = N; a.Hq = H_q; a.Hkv = c.H_kv; a.D = c.D; a.S_max = c.S_max;
+    a.kc = c.kc; a.ks = c.ks; a.vc = c.vc; a.vs = c.vs;
+    a.st_k = d_s_tensor_k; a.st_v = d_s_tensor_v;
+    a.start = d_start_pos; a.n_nodes = d_n_nodes;
+    a.mask = d_tree_mask; a.mask_stride = mask_stride;
+    a.softmax_scale = softmax_scale;
+    a.out = out;
+    a.partials = static_cast<float*>(workspace);
+    a.status = d_status;
+    a.block_table = c.block_table;
+    a.page_tokens = c.page_tokens; a.max_pages = c.max_pages; a.num_pages = c.num_pages;
+    a.wait_polls = g_wait_polls.load();
+    return from_cuda(launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+template <class Plane>
+nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int32_t* d_start_pos,
+                             const int32_t* d_path, const int32_t* d_n_accepted, int32_t* d_new_lens,
+                             int32_t* d_status, nvfp4_stream_t stream) {
+    if (n_planes < 0 || N < 0 || (n_planes > 0 && planes == nullptr)) return NVFP4_ERR_INVALID_ARG;
+    if (d_start_pos == nullptr || d_path == nullptr || d_n_accepted == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (d_new_lens != nullptr && (d_new_lens == d_start_pos || d_new_lens == d_n_accepted))
+        return NVFP4_ERR_INVALID_ARG;
+    if (N > kTreeMaxNodes) return NVFP4_ERR_UNSUPPORTED;
+    if (n_planes == 0) return NVFP4_OK;
+    CommitLaunch a{};
+    CachePair c{};
+    a.num_pages = INT32_MAX;
+    for (int i = 0; i < n_planes; ++i) {
+        if (!cache_pair(&planes[0], &planes[i], c)) return NVFP4_ERR_INVALID_ARG;
+        if (c.num_pages < a.num_pages) a.num_pages = c.num_pages;
+    }
+    if (c.B == 0 || N == 0) return NVFP4_OK;
+    a.planes = planes;
+    a.codes = [](const void* p, int i) { return static_cast<const Plane*>(p)[i].codes; };
+    a.scales = [](const void* p, int i) { return static_cast<const Plane*>(p)[i].scales; };
+    a.n_planes = n_planes;
+    a.start = d_start_pos; a.path = d_path; a.n_acc = d_n_accepted;
+    a.new_lens = d_new_lens; a.status = d_status;
+    a.block_table = c.block_table;
+    a.page_tokens = c.page_tokens; a.max_pages = c.max_pages;
+    a.B = c.B; a.Hkv = c.H_kv; a.S_max = c.S_max; a.D = c.D; a.N = N;
+    return from_cuda(launch_commit_path(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+#define NVFP4_NORM_ROPE_ENTRY(NAME, PLANE)                                                                            \
+    nvfp4_status NAME(const void* x_q, const void* x_k, const void* x_v, nvfp4_dtype dtype, int n_new, int H_q,       \
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* w_q, const void* w_k,         \
+                      float eps, const float* rope_table, int rope_positions, int rope_dims, int rope_interleaved,    \
+                      const int32_t* d_positions, const int32_t* d_start_pos, const int32_t* d_n_valid,               \
+                      int32_t* d_new_lens, const float* d_s_tensor_k, const float* d_s_tensor_v, const PLANE* k,      \
+                      const PLANE* v, void* q_out, int32_t* d_status, nvfp4_stream_t stream) {                        \
+        CachePair c{};                                                                                                \
+        if (!cache_pair(k, v, c)) return NVFP4_ERR_INVALID_ARG;                                                       \
+        return run_qk_norm_rope_append(x_q, x_k, x_v, dtype, n_new, H_q, q_stride, k_stride, v_stride, w_q, w_k, eps, \
+                                       rope_table, rope_positions, rope_dims, rope_interleaved, d_positions,          \
+                                       d_start_pos, d_n_valid, d_new_lens, d_s_tensor_k, d_s_tensor_v, c, q_out,      \
+                                       d_status, stream);                                                             \
+    }
+NVFP4_NORM_ROPE_ENTRY(nvfp4_qk_norm_rope_append, nvfp4_kv_plane)
+NVFP4_NORM_ROPE_ENTRY(nvfp4_qk_norm_rope_append_paged, nvfp4_kv_paged_plane)
+#undef NVFP4_NORM_ROPE_ENTRY
+
+size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D) {
+    if (B < 0 || N < 0 || N > kTreeMaxNodes || H_kv <= 0 || H_q <= 0 || (H_q % H_kv) != 0 || H_q / H_kv > 128) return 0;
+    if (D != 64 && D != 128) return 0;
+    return tree_attention_workspace(B, N, H_q, H_kv, D);
+}
+
+#define NVFP4_TREE_ENTRY(NAME, PLANE)                                                                                \
+    nvfp4_status NAME(const void* q, nvfp4_dtype q_dtype, int N, int H_q, const PLANE* k, const PLANE* v,            \
+                      const float* d_s_tensor_k, const float* d_s_tensor_v, const int32_t* d_start_pos,              \
+                      const int32_t* d_n_nodes, const int32_t* d_tree_mask, int64_t mask_stride,                     \
+                      float softmax_scale, void* out, nvfp4_dtype out_dtype, void* workspace,                        \
+                      size_t workspace_bytes, int32_t* d_status, nvfp4_stream_t stream) {                            \
+        CachePair c{};                                                                                               \
+        if (!cache_pair(k, v, c)) return NVFP4_ERR_INVALID_ARG;                                                      \
+        return run_tree_attention(q, q_dtype, N, H_q, c, d_s_tensor_k, d_s_tensor_v, d_start_pos, d_n_nodes,         \
+                                  d_tree_mask, mask_stride, softmax_scale, out, out_dtype, workspace,                \
+                                  workspace_bytes, d_status, stream);                                                \
+    }
+NVFP4_TREE_ENTRY(nvfp4_tree_attention, nvfp4_kv_plane)
+NVFP4_TREE_ENTRY(nvfp4_tree_attention_paged, nvfp4_kv_paged_plane)
+#undef NVFP4_TREE_ENTRY
+
+nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_probs, nvfp4_dtype dtype, int B, int N,
+                                 int V, const int32_t* d_tokens, const int32_t* d_parents, int parents_shared,
+                                 const float* d_u_accept, const float* d_u_sample, const int32_t* d_n_nodes,
+                                 int32_t* d_path, int32_t* d_n_accepted, int32_t* d_next_token, int32_t* d_status,
+                                 nvfp4_stream_t stream) {
+    if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
+    if (B < 0 || N <= 0 || V <= 0) return NVFP4_ERR_INVALID_ARG;
+    if (N > kTreeMaxNodes || B > (1 << 24)) return NVFP4_ERR_UNSUPPORTED;
+    if (B == 0) return NVFP4_OK;
+    if (target_probs == nullptr || d_tokens == nullptr || d_parents == nullptr || d_u_accept == nullptr ||
+        d_u_sample == nullptr || d_path == nullptr || d_n_accepted == nullptr || d_next_token == nullptr)
+        return NVFP4_ERR_INVALID_ARG;
+    const uintptr_t esz = dtype == NVFP4_IN_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(target_probs) % esz != 0 || reinterpret_cast<uintptr_t>(draft_probs) % esz != 0)
+        return NVFP4_ERR_INVALID_ARG;
+    VerifyLaunch a{};
+    a.p = target_probs; a.d = draft_probs;
+    a.f32 = dtype == NVFP4_IN_F32;
+    a.tokens = d_tokens; a.parents = d_parents;
+    a.parents_shared = parents_shared != 0;
+    a.u_accept = d_u_accept; a.u_sample = d_u_sample;
+    a.n_nodes = d_n_nodes;
+    a.path = d_path; a.n_acc = d_n_accepted; a.next = d_next_token; a.status = d_status;
+    a.B = B; a.N = N; a.V = V;
+    return from_cuda(launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_commit_path(const nvfp4_kv_plane* planes, int n_planes, int N, const int32_t* d_start_pos,
+                                  const int32_t* d_path, const int32_t* d_n_accepted, int32_t* d_new_lens,
+                                  int32_t* d_status, nvfp4_stream_t stream) {
+    return run_commit_path(planes, n_planes, N, d_start_pos, d_path, d_n_accepted, d_new_lens, d_status, stream);
+}
+
+nvfp4_status nvfp4_kv_commit_path_paged(const nvfp4_kv_paged_plane* planes, int n_planes, int N,
+                                        const int32_t* d_start_pos, const int32_t* d_path,
+                                        const int32_t* d_n_accepted, int32_t* d_new_lens, int32_t* d_status,
+                                        nvfp4_stream_t stream) {
+    return run_commit_path(planes, n_planes, N, d_start_pos, d_path, d_n_accepted, d_new_lens, d_status, stream);
+}
+
 }  // extern "C"

@@ -110,4 +110,76 @@ struct AttnWorkspace {
 };
 AttnWorkspace attention_workspace(int B, int Hq, int Hkv, int D);
 
+// ---- a step of tree-drafted decoding ----
+// nodes of a drafted tree (mask words, paths and node tables in shared memory)
+constexpr int kTreeMaxNodes = 1024;
+// planes one nvfp4_kv_commit_path launch moves (kernel parameters)
+constexpr int kCommitPlanes = 64;
+
+struct NormRopeLaunch {
+    const void *xq, *xk, *xv;
+    bool f32;
+    int64_t sq, sk, sv;          // elements between tokens
+    const void *wq, *wk;
+    const float* table;
+    const int32_t *positions, *start, *n_valid;
+    int32_t* new_lens;
+    const float *st_k, *st_v;
+    void* q_out;
+    uint8_t *kc, *ks, *vc, *vs;
+    const int32_t* block_table;  // nullptr: contiguous planes
+    int32_t* status;
+    int B, n, Hq, Hkv, D, S_max, R, P;
+    int page_tokens, max_pages, num_pages;
+    float eps;
+    bool interleaved;
+};
+cudaError_t launch_qk_norm_rope_append(const NormRopeLaunch& a, cudaStream_t stream);
+
+struct VerifyLaunch {
+    const void *p, *d;
+    bool f32;
+    const int32_t *tokens, *parents;
+    bool parents_shared;
+    const float *u_accept, *u_sample;
+    const int32_t* n_nodes;
+    int32_t *path, *n_acc, *next, *status;
+    int B, N, V;
+};
+cudaError_t launch_verify_drafts(const VerifyLaunch& a, cudaStream_t stream);
+
+struct CommitLaunch {
+    const void* planes;          // host array of nvfp4_kv_plane or nvfp4_kv_paged_plane
+    uint8_t* (*codes)(const void* planes, int i);
+    uint8_t* (*scales)(const void* planes, int i);
+    int n_planes;
+    const int32_t *start, *path, *n_acc;
+    int32_t *new_lens, *status;
+    const int32_t* block_table;
+    int num_pages, page_tokens, max_pages;
+    int B, Hkv, S_max, D, N;
+};
+cudaError_t launch_commit_path(const CommitLaunch& a, cudaStream_t stream);
+
+// attention of a drafted tree's nodes over the cache (tcgen05)
+struct TreeLaunch {
+    const void* q;
+    bool out_bf16;
+    int B, N, Hq, Hkv, D, S_max;
+    const uint8_t *kc, *ks, *vc, *vs;
+    const float *st_k, *st_v;
+    const int32_t *start, *n_nodes;
+    const int32_t* mask;         // nullptr: a chain
+    int64_t mask_stride;         // words between sequences, 0: one tree for all
+    float softmax_scale;
+    void* out;
+    float* partials;
+    int32_t* status;
+    const int32_t* block_table;
+    int page_tokens, max_pages, num_pages;
+    uint32_t wait_polls;
+};
+cudaError_t launch_tree_attention(const TreeLaunch& a, cudaStream_t stream);
+size_t tree_attention_workspace(int B, int N, int Hq, int Hkv, int D);
+
 }  // namespace nvfp4kv

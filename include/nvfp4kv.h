@@ -366,6 +366,162 @@ nvfp4_status nvfp4_decode_attention_noalloc(const void* q, nvfp4_dtype q_dtype, 
                                             const int32_t* d_seq_lens, float softmax_scale,
                                             float* out, int32_t* d_status, nvfp4_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A step of tree-drafted (speculative) decoding over the cache.  The pages
+ * describe no such step; these calls are for users who draft several tokens
+ * per sequence and let one pass of the model check them:
+ *
+ *   per layer  nvfp4_qk_norm_rope_append   the nodes' K/V into the cache, their queries out
+ *              nvfp4_tree_attention        every node attends its prefix and its ancestors
+ *   then       nvfp4_verify_drafts         which path of the tree is kept, and the next token
+ *   then       nvfp4_kv_commit_path        that path's slots move together, in every layer's planes
+ *
+ * The N nodes of sequence b sit at cache slots start_pos[b] .. start_pos[b] +
+ * N - 1 in node order; node 0 is the root (the last token sampled), and a node
+ * comes after its parent.  d_n_nodes (or d_n_valid), int32 [B] or NULL, gives
+ * the nodes of each sequence of a padded batch: what lies behind them is
+ * neither read nor written.  A count outside [0, N] skips its sequence and
+ * reports NVFP4_ERR_INVALID_ARG through *d_status.  N is at most 1024.
+ * ------------------------------------------------------------------------- */
+
+/* RMS norm of each query and key head, rotary position embedding and the
+ * quantize-append of K and V in one launch.  Per head row x of D elements
+ * (queries and keys; values are only quantized):
+ *     y   = x * r * w,  r = 1 / sqrt(mean(x^2) + eps)
+ *     (y_i, y_j) -> (y_i cos - y_j sin, y_j cos + y_i sin)
+ * each step one fp32 rounding.  The queries are rounded once to `dtype`; K and
+ * V are quantized from fp32 as by nvfp4_kv_quantize_append.
+ *   x_q, x_k, x_v  device [B][n_new][H_q or H_kv][D] of `dtype`, 16-byte
+ *                  aligned; *_stride: elements from one token to the next (0:
+ *                  dense), a multiple of 16 bytes, so that the three may be
+ *                  parts of one projection's output
+ *   w_q, w_k       device [D] of `dtype`, 16-byte aligned, or NULL (ones)
+ *   eps            >= 0; negative: no norm (w_q, w_k unused)
+ *   rope_table     device float [rope_positions][rope_dims], 16-byte aligned:
+ *                  rope_dims/2 cosines, then rope_dims/2 sines of a position;
+ *                  NULL with rope_dims 0: no rotation
+ *   rope_dims      a multiple of 16, at most D; the other dimensions pass
+ *   rope_interleaved  0: pairs (i, i + rope_dims/2); else pairs (2i, 2i + 1)
+ *   d_positions    device int32 [B][n_new], or NULL: start_pos[b] + i
+ *   d_start_pos    device int32 [B]: token i goes to slot start_pos[b] + i
+ *   d_n_valid      device int32 [B] or NULL: tokens of each sequence
+ *   d_new_lens     device int32 [B] or NULL: written with start + n_valid; must
+ *                  not alias d_start_pos or d_n_valid
+ *   q_out          device [B][n_new][H_q][D] of `dtype`, 16-byte aligned; must
+ *                  not overlap the inputs
+ * A sequence with start < 0 or start + n_valid > S_max is skipped entirely
+ * with NVFP4_ERR_CAPACITY; a position outside the table skips its token with
+ * NVFP4_ERR_INVALID_ARG; a bad tensor scale skips everything with
+ * NVFP4_ERR_NONFINITE.  Paged: a block-table entry outside the pool skips the
+ * token's K and V with NVFP4_ERR_INVALID_ARG. */
+nvfp4_status nvfp4_qk_norm_rope_append(const void* x_q, const void* x_k, const void* x_v, nvfp4_dtype dtype,
+                                       int n_new, int H_q, int64_t q_stride, int64_t k_stride,
+                                       int64_t v_stride, const void* w_q, const void* w_k, float eps,
+                                       const float* rope_table, int rope_positions, int rope_dims,
+                                       int rope_interleaved, const int32_t* d_positions,
+                                       const int32_t* d_start_pos, const int32_t* d_n_valid,
+                                       int32_t* d_new_lens, const float* d_s_tensor_k,
+                                       const float* d_s_tensor_v, const nvfp4_kv_plane* k,
+                                       const nvfp4_kv_plane* v, void* q_out, int32_t* d_status,
+                                       nvfp4_stream_t stream);
+nvfp4_status nvfp4_qk_norm_rope_append_paged(const void* x_q, const void* x_k, const void* x_v,
+                                             nvfp4_dtype dtype, int n_new, int H_q, int64_t q_stride,
+                                             int64_t k_stride, int64_t v_stride, const void* w_q,
+                                             const void* w_k, float eps, const float* rope_table,
+                                             int rope_positions, int rope_dims, int rope_interleaved,
+                                             const int32_t* d_positions, const int32_t* d_start_pos,
+                                             const int32_t* d_n_valid, int32_t* d_new_lens,
+                                             const float* d_s_tensor_k, const float* d_s_tensor_v,
+                                             const nvfp4_kv_paged_plane* k, const nvfp4_kv_paged_plane* v,
+                                             void* q_out, int32_t* d_status, nvfp4_stream_t stream);
+
+/* Workspace bytes of nvfp4_tree_attention on the current device (it depends on
+ * the SM count).  0 for invalid shapes.  The contents need no initialisation;
+ * calls that share one workspace must not overlap on the GPU. */
+size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D);
+
+/* Attention of a tree's nodes over the cache, their own K/V included: node i
+ * of sequence b sees every cache token t < start_pos[b], and node j's slot iff
+ * bit j of its mask row is set.  Tensor cores (tcgen05, f16 MMAs over the
+ * cache's FP8 values, fp32 accumulation and softmax statistics).
+ *   q            device [B][N][H_q][D] bf16, 16-byte aligned (fp32 queries:
+ *                NVFP4_ERR_UNSUPPORTED); H_q / H_kv <= 128
+ *   d_tree_mask  device int32: per node ceil(N / 32) words, bit j % 32 of word
+ *                j / 32 for node j (bits past the sequence's nodes are ignored);
+ *                NULL: a chain, node i sees nodes j <= i
+ *   mask_stride  words from one sequence's mask to the next; 0: one tree for all
+ *   softmax_scale  0 selects 1 / sqrt(D)
+ *   out          device [B][N][H_q][D] of out_dtype, 16-byte aligned.  fp32: the
+ *                probabilities enter the second product as two f16 terms (about
+ *                22 bits); bf16: as one, whose rounding (2^-11) is below the output's
+ *   workspace    >= nvfp4_tree_attention_workspace(...) bytes, 16-byte aligned
+ * A node that sees nothing gives a zero row.  A sequence with start_pos < 0 or
+ * start_pos + nodes > S_max is skipped with NVFP4_ERR_CAPACITY (its rows are
+ * left as they were).  Paged: as for nvfp4_decode_attention_paged. */
+nvfp4_status nvfp4_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H_q, const nvfp4_kv_plane* k,
+                                  const nvfp4_kv_plane* v, const float* d_s_tensor_k,
+                                  const float* d_s_tensor_v, const int32_t* d_start_pos,
+                                  const int32_t* d_n_nodes, const int32_t* d_tree_mask, int64_t mask_stride,
+                                  float softmax_scale, void* out, nvfp4_dtype out_dtype, void* workspace,
+                                  size_t workspace_bytes, int32_t* d_status, nvfp4_stream_t stream);
+nvfp4_status nvfp4_tree_attention_paged(const void* q, nvfp4_dtype q_dtype, int N, int H_q,
+                                        const nvfp4_kv_paged_plane* k, const nvfp4_kv_paged_plane* v,
+                                        const float* d_s_tensor_k, const float* d_s_tensor_v,
+                                        const int32_t* d_start_pos, const int32_t* d_n_nodes,
+                                        const int32_t* d_tree_mask, int64_t mask_stride, float softmax_scale,
+                                        void* out, nvfp4_dtype out_dtype, void* workspace,
+                                        size_t workspace_bytes, int32_t* d_status, nvfp4_stream_t stream);
+
+/* Verification of a tree's drafted tokens against the target's probabilities,
+ * from given random numbers.  The walk starts at node 0.  At node a, with
+ * w = p_a and Z = 1, each child c (token x) in node order:
+ *     accepted iff u_accept[c] * d_a(x) * Z < w(x): the walk goes on at c;
+ *     else w <- max(w - Z d_a, 0), Z <- sum w (both kept if that sum is 0).
+ * When no child is left the next token is the least i with
+ * w(0) + .. + w(i) > u_sample * sum w.  All of it in 64 bits.  With children
+ * drawn from d_a the tokens are distributed as the target's.
+ *   target_probs  device [B][N][V] of `dtype`: row i follows node i
+ *   draft_probs   device [B][N][V] of `dtype`: row i is what node i's children
+ *                 were drawn from; NULL: they were chosen, d_a is 1 at x, else 0
+ *   d_tokens      device int32 [B][N], in [0, V) (node 0's is unread)
+ *   d_parents     device int32 [B][N], or [N] when parents_shared; < the node
+ *   d_u_accept    device float [B][N]; d_u_sample device float [B]; in [0, 1)
+ *   d_path        device int32 [B][N]: the accepted nodes from node 0 on, then -1
+ *   d_n_accepted  device int32 [B]: nodes of the path (>= 1)
+ *   d_next_token  device int32 [B]
+ * NaN and negative probabilities count as 0.  A node with a bad token or
+ * parent is never accepted, with NVFP4_ERR_INVALID_ARG.  A last row without a
+ * positive finite sum gives token -1 and NVFP4_ERR_NONFINITE.  A sequence of
+ * 0 nodes is left as it was. */
+nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_probs, nvfp4_dtype dtype, int B,
+                                 int N, int V, const int32_t* d_tokens, const int32_t* d_parents,
+                                 int parents_shared, const float* d_u_accept, const float* d_u_sample,
+                                 const int32_t* d_n_nodes, int32_t* d_path, int32_t* d_n_accepted,
+                                 int32_t* d_next_token, int32_t* d_status, nvfp4_stream_t stream);
+
+/* Keep a tree's accepted path: in every given plane, slot start_pos[b] +
+ * path[b][j] moves to slot start_pos[b] + j for j < n_accepted[b], codes and
+ * scale bytes of all KV heads, as bytes.  One launch for up to 64 planes.
+ *   planes        host array of n_planes planes (all layers' K and V) that agree
+ *                 in B, H_kv, S_max and D (paged: in the block table too)
+ *   N             entries of a path row
+ *   d_path        device int32 [B][N], strictly increasing up to n_accepted
+ *   d_n_accepted  device int32 [B], 0 .. N
+ *   d_new_lens    device int32 [B] or NULL: start_pos + n_accepted; must not
+ *                 alias d_start_pos or d_n_accepted
+ * A sequence whose path is not increasing, or leaves [0, N), is skipped with
+ * NVFP4_ERR_INVALID_ARG; one that passes S_max with NVFP4_ERR_CAPACITY.
+ * Paged: a block-table entry outside the pool skips its node with
+ * NVFP4_ERR_INVALID_ARG. */
+nvfp4_status nvfp4_kv_commit_path(const nvfp4_kv_plane* planes, int n_planes, int N,
+                                  const int32_t* d_start_pos, const int32_t* d_path,
+                                  const int32_t* d_n_accepted, int32_t* d_new_lens, int32_t* d_status,
+                                  nvfp4_stream_t stream);
+nvfp4_status nvfp4_kv_commit_path_paged(const nvfp4_kv_paged_plane* planes, int n_planes, int N,
+                                        const int32_t* d_start_pos, const int32_t* d_path,
+                                        const int32_t* d_n_accepted, int32_t* d_new_lens, int32_t* d_status,
+                                        nvfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

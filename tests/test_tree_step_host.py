@@ -1,0 +1,167 @@
+"""Host-side checks of the tree-step entry points: every call below is refused,
+or is a no-op, before it reaches the GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import tree_reference as ref
+from bit_decode_attention_b200 import _native
+from bit_decode_attention_b200 import build as native_build
+
+INVALID, UNSUP, WS = _native.NVFP4_ERR_INVALID_ARG, _native.NVFP4_ERR_UNSUPPORTED, _native.NVFP4_ERR_WORKSPACE
+DEV = ctypes.c_void_p(256)      # never dereferenced
+ODD = ctypes.c_void_p(264)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    native_build.build()
+    return _native.lib()
+
+
+def plane(B=2, H=2, S=256, D=128, codes=256, scales=512):
+    return _native.KVPlaneStruct(codes, scales, B, H, S, D)
+
+
+def paged(codes=256, scales=512, table=1024, pages=4, H=2, T=128, D=128, B=2, M=3):
+    return _native.PagedPlaneStruct(codes, scales, table, pages, H, T, D, B, M)
+
+
+def norm_rope(lib, k=None, v=None, pg=False, **kw):
+    a = dict(xq=DEV, xk=DEV, xv=DEV, dt=0, n=1, hq=4, sq=0, sk=0, sv=0, wq=DEV, wk=DEV, eps=1e-6, table=DEV, P=64,
+             R=128, il=0, pos=None, start=DEV, valid=None, lens=None, stk=DEV, stv=DEV, out=DEV)
+    a.update(kw)
+    k = k or (paged() if pg else plane())
+    v = v or (paged() if pg else plane())
+    f = lib.nvfp4_qk_norm_rope_append_paged if pg else lib.nvfp4_qk_norm_rope_append
+    return f(a["xq"], a["xk"], a["xv"], a["dt"], a["n"], a["hq"], a["sq"], a["sk"], a["sv"], a["wq"], a["wk"],
+             ctypes.c_float(a["eps"]), a["table"], a["P"], a["R"], a["il"], a["pos"], a["start"], a["valid"], a["lens"],
+             a["stk"], a["stv"], ctypes.byref(k), ctypes.byref(v), a["out"], None, None)
+
+
+def test_norm_rope_append_refusals(lib):
+    for pg in (False, True):
+        for bad in (dict(dt=7), dict(n=-1), dict(hq=0), dict(stk=None), dict(stv=None), dict(start=None),
+                    dict(lens=DEV), dict(eps=float("nan")), dict(eps=float("inf")), dict(R=0), dict(R=24),
+                    dict(R=144), dict(P=0), dict(table=None), dict(table=ODD), dict(xq=None), dict(xq=ODD),
+                    dict(xk=ODD), dict(xv=None), dict(out=None), dict(out=ODD), dict(wq=ODD), dict(wk=ODD),
+                    dict(sq=508), dict(sq=516), dict(sk=260), dict(sv=8), dict(sk=-256),
+                    dict(valid=DEV, lens=DEV, start=ODD)):
+            assert norm_rope(lib, pg=pg, **bad) == INVALID, bad
+        assert norm_rope(lib, pg=pg, n=1 << 30) == UNSUP
+        assert norm_rope(lib, pg=pg, n=0) == 0
+    assert norm_rope(lib, v=plane(S=128)) == INVALID
+    assert norm_rope(lib, k=plane(D=96), v=plane(D=96)) == INVALID
+    assert norm_rope(lib, k=plane(B=0), v=plane(B=0)) == 0
+    assert norm_rope(lib, pg=True, v=paged(table=2048)) == INVALID     # K and V tables differ
+    assert norm_rope(lib, pg=True, k=paged(T=96), v=paged(T=96)) == INVALID
+
+
+def tree(lib, k=None, v=None, pg=False, **kw):
+    a = dict(q=DEV, dt=0, N=4, hq=4, stk=DEV, stv=DEV, start=DEV, nodes=None, mask=None, stride=0, scale=0.0, out=DEV,
+             odt=1, ws=DEV, nb=1 << 40)
+    a.update(kw)
+    k = k or (paged() if pg else plane())
+    v = v or (paged() if pg else plane())
+    f = lib.nvfp4_tree_attention_paged if pg else lib.nvfp4_tree_attention
+    return f(a["q"], a["dt"], a["N"], a["hq"], ctypes.byref(k), ctypes.byref(v), a["stk"], a["stv"], a["start"],
+             a["nodes"], a["mask"], a["stride"], ctypes.c_float(a["scale"]), a["out"], a["odt"], a["ws"], a["nb"],
+             None, None)
+
+
+def test_tree_attention_refusals(lib):
+    for pg in (False, True):
+        for bad in (dict(dt=7), dict(odt=7), dict(N=-1), dict(hq=3), dict(hq=0), dict(stk=None), dict(stv=None),
+                    dict(start=None), dict(scale=-1.0), dict(scale=float("nan")), dict(q=None), dict(q=ODD),
+                    dict(out=None), dict(out=ODD), dict(mask=DEV, stride=3), dict(mask=DEV, stride=-4)):
+            assert tree(lib, pg=pg, **bad) == INVALID, bad
+        for bad in (dict(dt=1), dict(N=1025), dict(hq=2 * 129)):
+            assert tree(lib, pg=pg, **bad) == UNSUP, bad
+        for bad in (dict(ws=None), dict(ws=ODD), dict(nb=16)):
+            assert tree(lib, pg=pg, **bad) == WS, bad
+        assert tree(lib, pg=pg, N=0) == 0
+    assert tree(lib, v=plane(S=128)) == INVALID
+    assert tree(lib, k=plane(B=0), v=plane(B=0)) == 0
+    # 2^9 sequences x 2^10 KV heads x 2^14 tiles of 128 tokens: past 31 bits
+    big = plane(B=512, H=1 << 10, S=1 << 21)
+    assert tree(lib, k=big, v=big, hq=1 << 10) == UNSUP
+    need = lib.nvfp4_tree_attention_workspace(2, 4, 4, 2, 128)
+    assert need > 0 and tree(lib, nb=need - 1) == WS
+    for shape in ((2, 4, 3, 2, 128), (2, 4, 4, 2, 96), (2, 1025, 4, 2, 128), (2, 4, 258, 2, 128), (-1, 4, 4, 2, 128)):
+        assert lib.nvfp4_tree_attention_workspace(*shape) == 0
+
+
+def test_verify_refusals(lib):
+    def call(p=DEV, d=DEV, dt=1, B=2, N=4, V=100, tok=DEV, par=DEV, sh=1, ua=DEV, us=DEV, path=DEV, na=DEV, nx=DEV):
+        return lib.nvfp4_verify_drafts(p, d, dt, B, N, V, tok, par, sh, ua, us, None, path, na, nx, None, None)
+    for bad in (dict(dt=7), dict(B=-1), dict(N=0), dict(V=0), dict(p=None), dict(tok=None), dict(par=None),
+                dict(ua=None), dict(us=None), dict(path=None), dict(na=None), dict(nx=None),
+                dict(p=ctypes.c_void_p(258)), dict(d=ctypes.c_void_p(258)), dict(dt=0, p=ctypes.c_void_p(257))):
+        assert call(**bad) == INVALID, bad
+    assert call(N=1025) == UNSUP
+    assert call(B=(1 << 24) + 1) == UNSUP
+    assert call(B=0) == 0
+
+
+def test_commit_refusals(lib):
+    def call(planes, n=None, N=4, start=DEV, path=DEV, na=ODD, lens=None, pg=False):
+        kind = _native.PagedPlaneStruct if pg else _native.KVPlaneStruct
+        arr = (kind * max(1, len(planes)))(*planes)
+        f = lib.nvfp4_kv_commit_path_paged if pg else lib.nvfp4_kv_commit_path
+        return f(arr, len(planes) if n is None else n, N, start, path, na, lens, None, None)
+    for pg, one, others in ((False, plane(), (plane(S=128), plane(H=4), plane(D=64), plane(B=3), plane(codes=257))),
+                            (True, paged(), (paged(table=2048), paged(T=256), paged(M=2), paged(pages=0)))):
+        for bad in (dict(start=None), dict(path=None), dict(na=None), dict(lens=DEV), dict(lens=ODD), dict(N=-1),
+                    dict(n=-1)):
+            assert call([one], pg=pg, **bad) == INVALID, bad
+        for o in others:
+            assert call([one, o], pg=pg) == INVALID
+        assert call([one], pg=pg, N=1025) == UNSUP
+        assert call([one], pg=pg, N=0) == 0
+        assert call([], pg=pg) == 0
+    assert call([plane(B=0)]) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes(lib, monkeypatch):
+    import bit_decode_attention_b200 as nv
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    pl = nv.KVPlane(torch.zeros(1, 1, 16, 64, dtype=torch.uint8), torch.zeros(1, 1, 16, 8, dtype=torch.uint8))
+    x = torch.zeros(1, 2, 1, 128, dtype=torch.bfloat16)
+    one = torch.ones(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.nvfp4_qk_norm_rope_append(x, x, x, i32(1), one, one, pl, pl)
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.nvfp4_tree_attention(x, pl, pl, one, one, i32(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.nvfp4_verify_drafts(torch.zeros(1, 2, 8), None, i32(1, 2), i32(2), torch.zeros(1, 2), one)
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.nvfp4_kv_commit_path([pl], i32(1), i32(1, 2), i32(1))
+    with pytest.raises(TypeError, match="PagedKVPlane"):
+        nv.nvfp4_tree_attention_paged(x, pl, pl, one, one, i32(1))
+    with pytest.raises(ValueError, match="at least one"):
+        nv.KVPlaneList([])
+
+
+def test_reference_forms_agree_with_closed_forms():
+    # the references the GPU tests compare with, on cases worked by hand
+    m = ref.ancestors(ref.parents_of("star", 4))
+    assert m.sum() == 7 and m[:, 0].all()
+    assert ref.mask_words(m).flatten().tolist() == [1, 3, 5, 9]
+    q = np.zeros((2, 1, 64))
+    kv = np.ones((1, 5, 64))
+    vv = np.arange(5.0)[None, :, None] * np.ones((1, 5, 64))
+    out, _, _, _ = ref.tree_attention(q, kv, vv, 3, 2, np.array([[True, False], [False, True]]))
+    assert np.allclose(out[0], (0 + 1 + 2 + 3) / 4) and np.allclose(out[1], (0 + 1 + 2 + 4) / 4)
+    # one token drafted with certainty: accepted with probability p(x); the rest is p without x
+    p = np.array([[0.5, 0.25, 0.25], [0.0, 0.0, 1.0]])
+    assert ref.verify(p, None, [0, 0], [-1, 0], [0, 0.49], 0.0, 2) == ([0, 1], 2)
+    assert ref.verify(p, None, [0, 0], [-1, 0], [0, 0.5], 0.5, 2) == ([0], 2)
+    assert ref.verify(p, None, [0, 0], [-1, 0], [0, 0.5], 0.49, 2) == ([0], 1)
+    d = np.array([[0.25, 0.75, 0.0], [0, 0, 1]])
+    assert ref.verify(p, d, [0, 1], [-1, 0], [0, 0.4], 0.49, 2) == ([0], 0)
+    y, _ = ref.norm_rope(np.array([3.0, 0, 4.0, 0] + [0.0] * 12), None, 0.0, np.array([0.0] * 8 + [1.0] * 8), True)
+    assert np.allclose(y[:4], [0, 3 / np.sqrt(25 / 16), 0, 4 / np.sqrt(25 / 16)])
