@@ -17,19 +17,48 @@
 // 128 rows, which share every dequantized tile.  Units cut by a range's end
 // leave partial (O, m, l) in the workspace; a second small kernel merges them.
 //
+// Two softmax groups of 128 threads work on alternate items, each with its own
+// scores S and accumulator O in tensor memory, so that one group's waits are the
+// other's work.  An item is one tile of the unit's rows (alternate tiles go to
+// alternate groups, whose (m, l, O) are merged when the unit ends); a unit of
+// more than 128 rows makes two items of every tile, a row block to each group.
+// Thread r of a group owns row r.  With 64 rows or fewer the rows stand 2 or 4
+// times among the 128, and each copy takes its part of the tile's tokens of the tile's tokens: the softmax's time falls with the rows, at no
+// cost to the MMAs, which multiply 128 rows anyway.  P . V of a copy's tokens writes
+// its lanes of O only (the others are disabled), so that nothing needs zeroing.
+//
 // Warp roles:
-//   warps 0-7    softmax: thread (h, r) owns tokens 64h .. 64h + 63 of score
-//                row r of a tile; the two halves exchange their maxima through shared
-//                memory (one 64-thread barrier per tile)
-//   warps 8-15   dequant: thread t of the first four warps owns token t's keys, of
-//                the others its values
-//   warp 16      bulk copies of raw codes and scales into the ring
-//   warp 17      MMA issue (one elected lane)
-//   warp 18      describes the unit this range cuts to the merge kernel
+//   warps 0-7    softmax, groups 0 and 1; they also load the queries
+//   warps 8-9    bulk copies of raw codes and scales into the ring: keys, values
+//   warp 10      MMA issue (one elected lane): O += P(i) . V, then S(i + 2)
+//   warps 12-    dequant, DG groups of eight warps; group i takes tiles i mod DG:
+//                thread t of its first four warps owns token t's keys, of the
+//                others its values
+//   warp 11      prefetch of the segments' queries into L2
 // P overwrites S in tensor memory, as the A operand of P . V: it takes no
-// shared memory.  S(i + 1) is issued before O += P(i) . V, so the scores of
-// the next item are ready when the softmax finishes one.
+// shared memory.
+//
+// What only the hardware signals (copies and MMAs that have ended) is an
+// mbarrier; what warps signal is a named barrier.  A wait that gives up sets
+// the CTA's abort flag; every role then runs through its loop without work, so
+// that all named barriers are met.
+//
+// Measured (B200, head_dim 128; a tile's raw bytes take 774 clocks of an SM's share
+// of 6.55 TB/s, its MMAs 512 with one row block and 1,024 with two):
+//   128 sequences x 8 KV heads, up to 8 nodes x 4 heads, 1,024 to 8,192 tokens:
+//     374 us, 2,140 clocks a tile; a loop of named waits paces it: dequant 2,300 to 2,900 (the SM issues
+//     0.59 instructions a clock and scheduler, the integer pipe is 58% busy), MMA
+//     issue and completion 1,000 until the buffer is free again, two buffers
+//   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 102 us, 4,700 clocks
+//     a tile; the softmax paces it: 3,300 of arithmetic (256 x 128 exponentials are
+//     2,048 at the SM's 16 a clock) and 1,400 between P and the next scores
+// Tried and slower on the first: rows on N (one exchange of maxima per tile: 394 us),
+// 8 dequant warps in place of 16 (451 us against 433 then), all 16 on each tile
+// (438 us), e4m3 keys with queries in two e4m3/e5m2 terms and a third value buffer
+// (377 us: 10% fewer integer instructions, more code than the instruction cache holds).
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_internal.h"
@@ -41,10 +70,9 @@ namespace nvfp4kv {
 namespace {
 
 constexpr int T = 128;                                // tokens per tile, rows per row block
-constexpr int kThreads = 20 * 32;
-constexpr int kDqWarp0 = 8, kLoadWarp = 16, kMmaWarp = 17, kDescWarp = 18;
-// registers after the prologue: 256 x 136 + 256 x 72 + 128 x 64 = 61,440 = 640 x 96
-constexpr uint32_t kRegsSoftmax = 136, kRegsDequant = 72, kRegsMisc = 64;
+constexpr int kLoadWarp = 8, kMmaWarp = 10, kDqWarp0 = 12;
+// named barriers (0: __syncthreads)
+constexpr int kBarSoftmax = 1, kBarK = 2, kBarV = 4, kBarP = 6, kBarDq = 8, kBarMeet = 12;
 constexpr uint32_t kTmemCols = 512;
 // O is rescaled only when a row's running max grows by more than 2^kSlack;
 // P = 2^(s - m + kBias) <= 2^14 stays inside f16, and weights down to 2^-30
@@ -53,8 +81,9 @@ constexpr float kSlack = 8.0f, kBias = 6.0f;
 constexpr int kLutCopies = 2;
 // fp32 outputs: the tensor core truncates its accumulator at every 16-token
 // step, a bias that grows with the context (1.6e-5 of the output at 128K
-// tokens); after this many tiles O is added, with rounding, to a second accumulator
-constexpr int kFlush = 8;
+// tokens).  After this many of a group's items O is added, with rounding, to an
+// fp32 sum in the workspace, and started again.
+constexpr int kFlush = 16;
 
 struct Params {
     const void* q;                                    // [B][N][Hq][D] bf16
@@ -64,6 +93,7 @@ struct Params {
     int64_t mask_stride;
     void* out;                                        // [B][N][Hq][D]
     float* partials;                                  // [2 * grid] slots
+    float* sums;                                      // [2 * grid][D][128]: flushed O of each group (fp32 outputs)
     int4* desc;                                       // [grid] units cut by a range's start
     int32_t* status;
     int32_t B, N, Hq, Hkv, g, S_max, W;               // W mask words per node
@@ -77,14 +107,23 @@ struct Params {
 template <int D_, int RB_>
 struct Cfg {
     static constexpr int D = D_, RB = RB_;
+    // Dequant groups of eight warps.  One takes 1,900 to 2,450 clocks a tile: less than
+    // two row blocks' softmax (3,400), whose threads the registers of a second group
+    // would be taken from; more than one block's (1,700 over two groups), where the
+    // second gains 4%.
+    static constexpr int DG = RB == 2 ? 1 : 2;
+    static constexpr int kThreads = 32 * (kDqWarp0 + 8 * DG);
+    // registers after the prologue: 256 x softmax + 128 x misc + 256 DG x dequant, of
+    // 640 x 96 = 61,440 or 896 x 72 = 64,512
+    static constexpr uint32_t kRegsSoftmax = DG == 1 ? 136 : 112, kRegsMisc = DG == 1 ? 64 : 56,
+                              kRegsDequant = DG == 1 ? 72 : 56;
     static constexpr int kCB = D / 2, kSB = D / 16;   // code / scale bytes per token
     static constexpr int kStage = T * (2 * kCB + 2 * kSB);
     static constexpr int kOffVC = T * kCB, kOffKS = 2 * T * kCB, kOffVS = 2 * T * kCB + T * kSB;
     static constexpr int kRing = RB == 2 && D == 128 ? 1 : 3;
     static constexpr int kTileBytes = T * D * 2;
-    static constexpr uint32_t kColO = 0, kColS = RB * D;
-    static constexpr uint32_t kColM = kColS + 2 * T;  // fp32 outputs (RB = 1): the sum of flushed O
-    static constexpr int kSlot = RB * T * (D + 2);    // floats of a partial: O, m, l
+    static constexpr uint32_t kColO = 0, kColS = 2 * D;   // of each group
+    static constexpr int kSlot = RB * T * (D + 2);    // floats of a partial: O [D/4][row][4], (m, l) [row]
 };
 
 // Canonical non-swizzled layouts (8 rows x 16 bytes per core matrix): K-major
@@ -97,19 +136,19 @@ struct __align__(1024) Smem {
     uint8_t v[2][C::kTileBytes];
     uint8_t ring[C::kRing][C::kStage];
     uint2 lut[2][128][kLutCopies];
-    float mx[2][2][T];                                // row maxima (and sums) of the two halves
+    float cs[C::RB][T];                               // score factor of a row
+    float ml[2][2][T];                                // m and l of each group's rows
     int32_t prefix[kMaxBatchPerLaunch + 1];
     int32_t warp_tot[16];
-    uint64_t full[C::kRing], empty[C::kRing];
-    uint64_t kready[2], kfree[2], vready[2], vfree[2], sready[2], pready[2];
-    uint64_t qready, oread, mma_done;
+    uint64_t full[2][C::kRing], empty[2][C::kRing];   // keys, values
+    uint64_t kfree[2], vfree[2], sready[2], pdone[2], qready, oread, mma_done;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
 
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&v)[64]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tc::tmem_ld_x16(addr + 16 * c, v + 16 * c);
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t* v) {
+    tc::tmem_st_x8(addr, v);
+    tc::tmem_st_x8(addr + 8, v + 8);
 }
 
 // STEPS kind::f16 MMAs (K = 16 each) with A and B in shared memory, the
@@ -132,17 +171,17 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 #undef NVFP4_SS_STEP
 }
 
-// Eight kind::f16 MMAs over 128 tokens with A = P in tensor memory: tokens
-// 0-63 in columns a .. a + 31, tokens 64-127 in a + 64 .. a + 95.
-__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-#define NVFP4_TS_STEP(INC) "add.u32 %1, %1, " INC ";\n\tadd.s64 %2, %2, 16;\n\t" \
-                           "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p1;\n\t"
+// Two kind::f16 MMAs over 32 tokens with A = P in tensor memory, columns a .. a + 15,
+// into the lanes that off[] does not name (a bit per lane of D).
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                       const uint32_t (&off)[4]) {
     asm volatile("{\n\t.reg .pred p0, p1;\n\tsetp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
-                 NVFP4_TS_STEP("8") NVFP4_TS_STEP("8") NVFP4_TS_STEP("8") NVFP4_TS_STEP("40")
-                 NVFP4_TS_STEP("8") NVFP4_TS_STEP("8") NVFP4_TS_STEP("8") "}"
-                 : "+r"(d), "+r"(a), "+l"(b) : "r"(idesc), "r"(acc) : "memory");
-#undef NVFP4_TS_STEP
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p0;\n\t"
+                 "add.u32 %1, %1, 8;\n\tadd.s64 %2, %2, 16;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p1;\n\t}"
+                 : "+r"(d), "+r"(a), "+l"(b)
+                 : "r"(idesc), "r"(acc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+                 : "memory");
 }
 
 template <uint32_t N>
@@ -154,18 +193,20 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Barrier of the two warps that share 32 rows; true when both pass true.  They
-// meet once per item whatever their waits gave, so that neither is left alone.
-__device__ __forceinline__ bool pair_and(int id, bool ok) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
-        "barrier.cta.red.and.aligned.pred b, %2, 64, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"(ok ? 1u : 0u), "r"(id)
-        : "memory");
-    return r != 0;
+// Named barriers: wait with n threads; arrive without waiting.  What a warp
+// did before (fenced for the async proxy where the tensor cores read it) comes
+// before what a warp that waits does after.
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
+// What a producer tells a consumer warp: it arrives, since its buffers' mbarriers
+// keep it from doing so twice before the consumer has met the first.  Once the
+// abort flag is up those waits are skipped, and it waits here instead.
+__device__ __forceinline__ void bar_tell(int id, int n, const int32_t* abort_flag) {
+    if (*reinterpret_cast<const volatile int32_t*>(abort_flag) != 0) bar_sync(id, n);
+    else asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void softmax_sync() { bar_sync(kBarSoftmax, 256); }
 
 __device__ __forceinline__ uint4 dequant8(uint32_t x, uint2 l) {
     uint32_t lo, hi;
@@ -197,6 +238,9 @@ struct Segment {
     int start, nodes, rows;                           // rows of this unit
     int tile0, tiles, unit_tiles;
 };
+
+// log2 of the copies of a unit's rows
+__device__ __forceinline__ int lg_copies(int rows) { return rows > 64 ? 0 : (rows > 32 ? 1 : 2); }
 
 template <class C>
 struct Walker {
@@ -257,7 +301,7 @@ __device__ __forceinline__ uint64_t visible64(const Params& p, const Segment& s,
 }
 
 template <class C, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const __grid_constant__ Params p) {
     constexpr int D = C::D, RB = C::RB;
     extern __shared__ uint8_t smem_raw[];
     Smem<C>& sm = *reinterpret_cast<Smem<C>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -271,19 +315,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __
     }
     if (warp == kLoadWarp && lane == 0) {
         for (int s = 0; s < C::kRing; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 256);
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(&sm.full[kv][s], 1);
+                mbar_init(&sm.empty[kv][s], 4);
+            }
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.kready[s], 128);
             mbar_init(&sm.kfree[s], 1);
-            mbar_init(&sm.vready[s], 128);
             mbar_init(&sm.vfree[s], 1);
             mbar_init(&sm.sready[s], 1);
-            mbar_init(&sm.pready[s], 256);
+            mbar_init(&sm.pdone[s], 1);
         }
-        mbar_init(&sm.qready, 256);
-        mbar_init(&sm.oread, 256);
+        mbar_init(&sm.qready, 1);
+        mbar_init(&sm.oread, 1);
         mbar_init(&sm.mma_done, 1);
         fence_mbar_init();
         sm.abort_flag = 0;
@@ -293,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __
         const int plane = tid >> 7;
         const uint2 w = lut_words((uint32_t)(tid & 127), plane ? st_v : st_k);
 #pragma unroll
-        for (int c = 0; c < kLutCopies; ++c) sm.lut[plane][tid & 127][c] = w;
+        for (int c = 0; c < kLutCopies; ++c)          // lanes rotated over the banks
+            sm.lut[plane][tid & 127][(c + lane) & (kLutCopies - 1)] = w;
     }
     if (tid == 0 && blockIdx.x == 0) {
         const bool ok = st_k > 0.f && st_k <= 3.4028234663852886e38f && st_v > 0.f && st_v <= 3.4028234663852886e38f;
@@ -335,18 +380,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __
     auto range_start = [&](int c) -> int { return (int)((int64_t)total * (c < nr ? c : nr) / nr); };
     const int lo = range_start((int)blockIdx.x), hi = range_start((int)blockIdx.x + 1);
 
-    if (warp >= kLoadWarp) {
-        regs_dec<kRegsMisc>();
-        if (warp == kLoadWarp && lane == 0) {
-            // ================= bulk copies, one stage per tile =================
+    if (warp >= kLoadWarp && warp < kDqWarp0) {
+        regs_dec<C::kRegsMisc>();
+        if (warp < kLoadWarp + 2 && lane == 0) {
+            // ================= bulk copies, one stage per tile: keys or values =================
+            const int which = warp - kLoadWarp;
+            uint64_t* const full = sm.full[which];
+            uint64_t* const empty = sm.empty[which];
+            const uint8_t* const codes = which ? p.vc : p.kc;
+            const uint8_t* const scales = which ? p.vs : p.ks;
             uint32_t n = 0;                           // tiles issued
             bool ok = true;
             Walker<C> w(lo, hi);
             Segment s;
             while (ok && w.next(p, sm.prefix, s)) {
+#pragma unroll 1
                 for (int k = 0; k < s.tiles; ++k, ++n) {
                     const int st = n % C::kRing;
-                    if (n >= C::kRing && !wait_one(&sm.empty[st], (n / C::kRing - 1) & 1, abort_flag, p.status, polls)) {
+                    if (n >= C::kRing && !wait_one(&empty[st], (n / C::kRing - 1) & 1, abort_flag, p.status, polls)) {
                         ok = false;
                         break;
                     }
@@ -366,17 +417,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __
                         tok = ((int64_t)page * p.Hkv + s.hk) * p.page_tokens + (t0 - lp * p.page_tokens);
                     }
                     const uint32_t cb = (uint32_t)ncopy * C::kCB, sb = (uint32_t)ncopy * C::kSB;
-                    mbar_arrive_expect_tx(&sm.full[st], 2 * (cb + sb));
-                    uint8_t* dst = sm.ring[st];
-                    bulk_g2s(dst, p.kc + tok * C::kCB, cb, &sm.full[st]);
-                    bulk_g2s(dst + C::kOffKS, p.ks + tok * C::kSB, sb, &sm.full[st]);
-                    bulk_g2s(dst + C::kOffVC, p.vc + tok * C::kCB, cb, &sm.full[st]);
-                    bulk_g2s(dst + C::kOffVS, p.vs + tok * C::kSB, sb, &sm.full[st]);
+                    mbar_arrive_expect_tx(&full[st], cb + sb);
+                    bulk_g2s(sm.ring[st] + (which ? C::kOffVC : 0), codes + tok * C::kCB, cb, &full[st]);
+                    bulk_g2s(sm.ring[st] + (which ? C::kOffVS : C::kOffKS), scales + tok * C::kSB, sb, &full[st]);
                 }
+            }
+            // ---- the unit that this range's start cuts first is merged by block
+            // blockIdx.x: contributors and rows, sequence, KV head, row unit ----
+            if (which == 0) {
+                int4 d = make_int4(0, 0, 0, 0);
+                Walker<C> w0(lo, hi);
+                if (w0.next(p, sm.prefix, s) && s.tile0 > 0 && lo - s.tile0 >= range_start((int)blockIdx.x - 1)) {
+                    int c = (int)blockIdx.x + 1;      // ranges blockIdx.x - 1 .. c - 1 hold tiles of it
+#pragma unroll 1
+                    while (c < nr && range_start(c) < lo - s.tile0 + s.unit_tiles) ++c;
+                    d = make_int4((c - (int)blockIdx.x + 1) | s.rows << 16, s.b, s.hk, s.ru);
+                }
+                p.desc[blockIdx.x] = d;
             }
             // every issued copy lands before the CTA exits
             for (uint32_t i = n > C::kRing ? n - C::kRing : 0; i < n; ++i)
-                if (!mbar_wait_sleep(&sm.full[i % C::kRing], (i / C::kRing) & 1, 1u << 16)) {
+                if (!mbar_wait_sleep(&full[i % C::kRing], (i / C::kRing) & 1, 1u << 16)) {
                     report(p.status, NVFP4_ERR_TIMEOUT);
                     break;
                 }
@@ -388,353 +449,415 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_tc_kernel(const __
             bool ok = true;
             Walker<C> w(lo, hi);
             Segment s;
-            while (ok && w.next(p, sm.prefix, s)) {
-                const int nrb = RB == 2 && s.rows > T ? 2 : 1;
-                const int items = s.tiles * nrb;
-                ok = wait_warp(&sm.qready, seg & 1, abort_flag, p.status, polls);
-                // S(i) = Q . K^T into buffer (gi + i) % 2
-                auto issue_qk = [&](int i) -> bool {
-                    const int tile = RB == 2 && nrb == 2 ? i >> 1 : i, rb = RB == 2 && nrb == 2 ? i & 1 : 0;
-                    const uint32_t kt = gt + tile, kb = kt & 1;
-                    if (rb == 0 && !wait_warp(&sm.kready[kb], (kt >> 1) & 1, abort_flag, p.status, polls)) return false;
+            for (; w.next(p, sm.prefix, s); ++seg) {
+                const int dual = RB == 2 && s.rows > T ? 1 : 0;
+                const int items = s.tiles << dual;
+                const int lg_parts = lg_copies(s.rows);
+                ok = wait_warp(&sm.qready, seg & 1, abort_flag, p.status, polls) && ok;
+                // S(i) = Q . K^T of group (gi + i) % 2.  (P(i - 2), which lay there, has been
+                // read by an MMA issued before.)
+                auto issue_qk = [&](int i) {
+                    const uint32_t grp = (gi + i) & 1, kt = gt + (i >> dual), kb = kt & 1;
+                    if (!dual || !(i & 1)) bar_sync(kBarK + kb, 160);
                     tc::fence_after_sync();
-                    if (tc::elect_one()) {
-                        mma_ss<D / 16>(tbase + C::kColS + T * ((gi + i) & 1),
-                                       tc::smem_desc(tc::smem_addr(sm.q[rb]), 128, 16 * D),
+                    if (ok && tc::elect_one()) {
+                        mma_ss<D / 16>(tbase + C::kColS + T * grp,
+                                       tc::smem_desc(tc::smem_addr(sm.q[dual ? grp : 0]), 128, 16 * D),
                                        tc::smem_desc(tc::smem_addr(sm.k[kb]), 128, 16 * D), idesc_qk);
-                        tc::mma_commit(&sm.sready[(gi + i) & 1]);
-                        if (rb == nrb - 1) tc::mma_commit(&sm.kfree[kb]);
+                        tc::mma_commit(&sm.sready[grp]);
+                        if (!dual || (i & 1)) tc::mma_commit(&sm.kfree[kb]);
                     }
                     __syncwarp();
-                    return true;
                 };
-                if (ok) ok = issue_qk(0);
-                for (int i = 0; ok && i < items; ++i) {
-                    if (i + 1 < items && !issue_qk(i + 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const int tile = RB == 2 && nrb == 2 ? i >> 1 : i, rb = RB == 2 && nrb == 2 ? i & 1 : 0;
-                    const uint32_t x = gi + i, vt = gt + tile, vb = vt & 1;
-                    if (!wait_warp(&sm.pready[x & 1], (x >> 1) & 1, abort_flag, p.status, polls) ||
-                        (rb == 0 && !wait_warp(&sm.vready[vb], (vt >> 1) & 1, abort_flag, p.status, polls)) ||
-                        // the previous segment's O has been read
-                        (i == 0 && seg > 0 && !wait_warp(&sm.oread, (seg - 1) & 1, abort_flag, p.status, polls))) {
-                        ok = false;
-                        break;
-                    }
+                issue_qk(0);
+                if (items > 1) issue_qk(1);
+#pragma unroll 1
+                for (int i = 0; i < items; ++i) {
+                    const uint32_t grp = (gi + i) & 1, vt = gt + (i >> dual), vb = vt & 1;
+                    if (!dual || !(i & 1)) bar_sync(kBarV + vb, 160);
+                    if (i == 0 && seg > 0)            // the previous segment's O has been read
+                        ok = wait_warp(&sm.oread, (seg - 1) & 1, abort_flag, p.status, polls) && ok;
+                    bar_sync(kBarP + grp, 160);
                     tc::fence_after_sync();
-                    if (tc::elect_one()) {
+                    if (ok && tc::elect_one()) {
                         const uint64_t dv = tc::smem_desc(tc::smem_addr(sm.v[vb]), 128, 2048);
-                        const uint32_t a = tbase + C::kColS + T * (x & 1), o = tbase + C::kColO + D * rb;
-                        mma_pv(o, a, dv, idesc_pv, (TWO ? tile % kFlush : tile) > 0 ? 1u : 0u);
-                        if (TWO) mma_pv(o, a + 32, dv, idesc_pv, 1u);
-                        if (rb == nrb - 1) tc::mma_commit(&sm.vfree[vb]);
+                        const uint32_t a = tbase + C::kColS + T * grp, o = tbase + C::kColO + D * grp;
+                        const int j = i >> 1;         // the group's items of this segment before
+                        const uint32_t acc = (TWO ? j % kFlush : j) > 0 ? 1u : 0u;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // the lanes of the copy that takes these 32 tokens
+                            const int lg_cpp = 2 - lg_parts;   // chunks of a copy
+                            uint32_t off[4];
+#pragma unroll
+                            for (int l = 0; l < 4; ++l) off[l] = l >> lg_cpp == c >> lg_cpp ? 0u : 0xFFFFFFFFu;
+                            const uint32_t first = c & ((1 << lg_cpp) - 1);
+                            mma_pv(o, a + 32 * c, dv + 32 * c, idesc_pv, first > 0 ? 1u : acc, off);
+                            if (TWO) mma_pv(o, a + 32 * c + 16, dv + 32 * c, idesc_pv, 1u, off);
+                        }
+                        tc::mma_commit(&sm.pdone[grp]);
+                        if (!dual || (i & 1)) tc::mma_commit(&sm.vfree[vb]);
                     }
                     __syncwarp();
+                    if (i + 2 < items) issue_qk(i + 2);
                 }
                 gi += items;
                 gt += s.tiles;
-                ++seg;
             }
             if (tc::elect_one()) tc::mma_commit(&sm.mma_done);
             __syncwarp();
-        } else if (warp == kDescWarp && lane == 0) {
-            // ================= the unit that this range's start cuts first =================
-            // is merged by block blockIdx.x: contributors, sequence, KV head, row unit
-            int4 d = make_int4(0, 0, 0, 0);
+        }
+        else if (warp == kMmaWarp + 1) {
+            // ================= the segments' queries, node by node, into L2 =================
             Walker<C> w(lo, hi);
             Segment s;
-            if (w.next(p, sm.prefix, s) && s.tile0 > 0 && lo - s.tile0 >= range_start((int)blockIdx.x - 1)) {
-                int c = (int)blockIdx.x + 1;          // ranges blockIdx.x - 1 .. c - 1 hold tiles of it
-                while (c < nr && range_start(c) < lo - s.tile0 + s.unit_tiles) ++c;
-                d = make_int4(c - (int)blockIdx.x + 1, s.b, s.hk, s.ru);
+            while (w.next(p, sm.prefix, s)) {
+                const int gr0 = s.ru * RB * T, nd0 = (int)p.fd_g.div((uint32_t)gr0),
+                          nd1 = (int)p.fd_g.div((uint32_t)(gr0 + s.rows - 1));
+                for (int nd = nd0 + lane; nd <= nd1; nd += 32) {
+                    const int first = max(gr0 - nd * p.g, 0), end = min(p.g, gr0 + s.rows - nd * p.g);
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                     reinterpret_cast<const uint16_t*>(p.q) +
+                                     (((int64_t)s.b * p.N + nd) * p.Hq + (int64_t)s.hk * p.g + first) * D),
+                                 "r"((end - first) * D * 2)
+                                 : "memory");
+                }
             }
-            p.desc[blockIdx.x] = d;
         }
     } else if (warp >= kDqWarp0) {
         // ================= dequant: token t of each tile, keys or values =================
-        regs_dec<kRegsDequant>();
-        const int which = (warp - kDqWarp0) >> 2;     // 0: keys, 1: values
+        regs_dec<C::kRegsDequant>();
+        const int which = ((warp - kDqWarp0) >> 2) & 1;   // 0: keys, 1: values
+        const int group = (warp - kDqWarp0) >> 3, bar = kBarDq + ((warp - kDqWarp0) >> 2);
         const int t = tid & (T - 1);
         const uint2* lut = &sm.lut[which][0][lane & (kLutCopies - 1)];
-        uint64_t* const ready = which ? sm.vready : sm.kready;
-        uint64_t* const free_ = which ? sm.vfree : sm.kfree;
-        uint32_t n = 0;
+        const bool poller = (warp & 3) == 0;
         constexpr int NCH = D / 32;                   // 16-byte code chunks of a token
         const uint32_t ntiles = (uint32_t)(hi - lo);  // every tile of the range once, in order
-        for (; n < ntiles; ++n) {
-            const int st = n % C::kRing;
-            if (!wait_warp(&sm.full[st], (n / C::kRing) & 1, abort_flag, p.status, polls)) break;
-            const uint8_t* raw = sm.ring[st] + (which ? C::kOffVC : 0) + t * C::kCB;
-            // chunk order rotated per thread: eight lanes read eight different 16-byte banks
-            uint4 code[NCH];
-            const int rot = D == 128 ? (t >> 1) : (t >> 2);
-#pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                code[j] = *reinterpret_cast<const uint4*>(raw + 16 * ((j + rot) & (NCH - 1)));
-            uint32_t sb[2];
-            const uint8_t* sraw = sm.ring[st] + (which ? C::kOffVS : C::kOffKS) + t * C::kSB;
-            if (D == 128) {
-                const uint2 u = *reinterpret_cast<const uint2*>(sraw);
-                sb[0] = u.x;
-                sb[1] = u.y;
-            } else {
-                sb[0] = sb[1] = *reinterpret_cast<const uint32_t*>(sraw);
+#pragma unroll 1
+        for (uint32_t n = group; n < ntiles; n += C::DG) {
+            const uint32_t st = n % C::kRing, buf = n & 1;
+            if (poller) {
+                wait_warp(&sm.full[which][st], (n / C::kRing) & 1, abort_flag, p.status, polls);
+                // the MMAs of the buffer's last tile have read it
+                if (n >= 2)
+                    wait_warp(which ? &sm.vfree[buf] : &sm.kfree[buf], ((n >> 1) - 1) & 1, abort_flag, p.status, polls);
             }
-            fence_proxy_async_smem();                 // the next copy into this stage comes after these reads
-            mbar_arrive(&sm.empty[st]);
-            const uint32_t buf = n & 1;
-            if (n >= 2 && !wait_warp(&free_[buf], ((n >> 1) - 1) & 1, abort_flag, p.status, polls)) break;
+            bar_sync(bar, 128);
+            const uint8_t* raw = sm.ring[st] + (which ? C::kOffVC : 0) + t * C::kCB;
+            const uint8_t* sraw = sm.ring[st] + (which ? C::kOffVS : C::kOffKS) + t * C::kSB;
             uint8_t* dst = which ? sm.v[buf] + (t / 8) * 128 + (t % 8) * 16 : sm.k[buf] + (t / 8) * (16 * D) + (t % 8) * 16;
             const int step = which ? 2048 : 128;      // between 8-element groups of the head dimension
-#pragma unroll
+            // chunk order rotated per thread: eight lanes read eight different 16-byte
+            // banks.  The loop stays rolled: the roles' loops together have to fit the
+            // instruction cache.
+            const int rot = D == 128 ? (t >> 1) : (t >> 2);
+#pragma unroll 1
             for (int j = 0; j < NCH; ++j) {
                 const int c = (j + rot) & (NCH - 1);
-                const uint32_t two = (D == 128 && (c & 2) ? sb[1] : sb[0]) >> (16 * (c & 1));
+                const uint4 code = *reinterpret_cast<const uint4*>(raw + 16 * c);
+                const uint32_t two = *reinterpret_cast<const uint16_t*>(sraw + 2 * c);
                 const uint2 la = lut[(two & 0x7F) * kLutCopies];
-                const uint2 lb = lut[((two >> 8) & 0x7F) * kLutCopies];
-                uint8_t* d8 = dst + 4 * c * step;
-                *reinterpret_cast<uint4*>(d8) = dequant8(code[j].x, la);
-                *reinterpret_cast<uint4*>(d8 + step) = dequant8(code[j].y, la);
-                *reinterpret_cast<uint4*>(d8 + 2 * step) = dequant8(code[j].z, lb);
-                *reinterpret_cast<uint4*>(d8 + 3 * step) = dequant8(code[j].w, lb);
+                const uint2 lb = lut[(two >> 8 & 0x7F) * kLutCopies];
+                uint8_t* const d8 = dst + 4 * c * step;
+                *reinterpret_cast<uint4*>(d8) = dequant8(code.x, la);
+                *reinterpret_cast<uint4*>(d8 + step) = dequant8(code.y, la);
+                *reinterpret_cast<uint4*>(d8 + 2 * step) = dequant8(code.z, lb);
+                *reinterpret_cast<uint4*>(d8 + 3 * step) = dequant8(code.w, lb);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&ready[buf]);
+            bar_tell((which ? kBarV : kBarK) + (int)buf, 160, abort_flag);
+            // this warp has read (and used) what it needs of the stage
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[which][st]);
         }
     } else {
-        // ================= softmax: tokens 64h .. 64h + 63 of row r =================
-        regs_inc<kRegsSoftmax>();
+        // ================= softmax: row r (or its copy) of the group's items =================
+        regs_inc<C::kRegsSoftmax>();
         const int h = warp >> 2, r = tid & (T - 1);
         const uint32_t trow = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
-        const int bar = 1 + (warp & 3);
-        constexpr int DH = D / 2;                     // columns of O this thread rescales and stores
-        uint32_t gi = 0, gt = 0;
-        bool ok = true;
+        const uint32_t scol = trow + C::kColS + T * h, ocol = trow + C::kColO + D * h;
+        float* const sums = TWO ? p.sums + (int64_t)(2 * blockIdx.x + h) * D * T + r : nullptr;
+        uint32_t gi = 0, seg = 0;
         Walker<C> w(lo, hi);
         Segment s;
-        while (ok && w.next(p, sm.prefix, s)) {
-            const int nrb = RB == 2 && s.rows > T ? 2 : 1;
-            float cs[RB], m_run[RB], l_run[RB];
-            int node[RB];
-            // query operand: q * 2^e rounded to f16, e from the row's amax
+#pragma unroll 1
+        for (; w.next(p, sm.prefix, s); ++seg) {
+            const int dual = RB == 2 && s.rows > T ? 1 : 0;
+            // copies of the rows, and tokens of a tile each takes: 128, 64 or 32
+            const int lg_parts = lg_copies(s.rows);
+            const int rows_per = T >> lg_parts, part = r >> (7 - lg_parts), lr = r & (rows_per - 1);
+            const int gr0 = s.ru * RB * T;
+            // ---- query operand: q * 2^e rounded to f16, e from the row's amax ----
+            {
+                // Lanes: 8 rows x 4 quarters of every 32 columns, so that eight lanes write
+                // 128 contiguous bytes of the operand; all of a row's loads are in flight.
+                constexpr int NP = D / 32;
+                const int quarter = lane >> 3;
+                const int rows = dual ? 2 * T : rows_per, copies = dual ? 1 : 1 << lg_parts;
+                const uint16_t* qh = reinterpret_cast<const uint16_t*>(p.q) +
+                                     ((int64_t)s.b * p.N * p.Hq + (int64_t)s.hk * p.g) * D + 8 * quarter;
+#pragma unroll 1
+                for (int row = 8 * warp + (lane & 7); row < rows; row += 64) {   // (a warp's rows: all or none)
+                    uint32_t x[4 * NP];
+                    const int gr = gr0 + row, qn = (int)p.fd_g.div((uint32_t)gr);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                m_run[rb] = -INFINITY;
-                l_run[rb] = 0.0f;
-                cs[rb] = 0.0f;
-                node[rb] = 0;
-                if (rb >= nrb) continue;
-                const int row = rb * T + r;
-                const bool live = row < s.rows;
-                const int gr = s.ru * RB * T + row;
-                const int nd = live ? (int)p.fd_g.div((uint32_t)gr) : 0;
-                node[rb] = nd;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    reinterpret_cast<const uint16_t*>(p.q) +
-                    (((int64_t)s.b * p.N + nd) * p.Hq + (int64_t)s.hk * p.g + (gr - nd * p.g)) * D);
-                uint32_t amax = 0;
-                if (live)
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 u = __ldg(src + c);
-                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            amax = max(amax, max((x[j] & 0x7FFFu) << 16, x[j] & 0x7FFF0000u));
+                    for (int k = 0; k < NP; ++k) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row < s.rows)
+                            u = __ldg(reinterpret_cast<const uint4*>(qh + ((int64_t)qn * p.Hq + (gr - qn * p.g)) * D + 32 * k));
+                        x[4 * k] = u.x; x[4 * k + 1] = u.y; x[4 * k + 2] = u.z; x[4 * k + 3] = u.w;
                     }
-                int e = 0;
-                if (amax > 0u && amax < 0x7F800000u) {
-                    int ex;
-                    frexpf(__uint_as_float(amax), &ex);
-                    e = 15 - ex;
-                    e = e < -126 ? -126 : (e > 126 ? 126 : e);
-                }
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                uint8_t* qd = sm.q[rb] + (r / 8) * (16 * D) + (r % 8) * 16;
-                for (int c = h * (D / 16); c < (h + 1) * (D / 16); ++c) {
-                    uint4 u = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t amax = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4 * NP; ++j) amax = max(amax, max((x[j] & 0x7FFFu) << 16, x[j] & 0x7FFF0000u));
+                    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+                    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 16));
+                    int e = 0;
+                    if (amax > 0u && amax < 0x7F800000u) {
+                        // amax < 2^(ex + 1); a subnormal takes the largest shift
+                        e = 14 - ((int)(amax >> 23) - 127);
+                        e = e < -126 ? -126 : (e > 126 ? 126 : e);
+                    }
+                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                    const float cs = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.17549435e-38f);
+#pragma unroll
+                    for (int j = 0; j < 4 * NP; ++j)
                         x[j] = pack_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up);
-                    *reinterpret_cast<uint4*>(qd + c * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll 1
+                    for (int c = 0; c < copies; ++c) {
+                        const int at = row + c * rows, rb = at >> 7;
+                        uint8_t* d8 = sm.q[rb] + ((at & 127) / 8) * (16 * D) + quarter * 128 + (at % 8) * 16;
+#pragma unroll
+                        for (int k = 0; k < NP; ++k)
+                            *reinterpret_cast<uint4*>(d8 + 512 * k) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                        if (quarter == 0) sm.cs[rb][at & 127] = cs;
+                    }
                 }
-                cs[rb] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.17549435e-38f);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&sm.qready);
+            softmax_sync();
+            if (tid == 0) mbar_arrive(&sm.qready);
 
-            for (int k = 0; ok && k < s.tiles; ++k) {
-                const int t0 = (s.tile0 + k) * T;
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    if (rb >= nrb) break;
-                    const uint32_t sb = gi & 1;
-                    ok = ok && wait_warp(&sm.sready[sb], (gi >> 1) & 1, abort_flag, p.status, polls);
-                    tc::fence_after_sync();
-                    // a warp without live rows leaves P as it is: it only reaches its own rows of O
-                    if (rb * T + 32 * (warp & 3) >= s.rows) {
-                        if (!ok) break;
-                    } else {
-                        uint32_t v[64];
-                        const uint32_t scol = trow + C::kColS + T * sb + 64 * h;
-                        tmem_ld64(scol, v);
+            const int row = dual ? T * h + r : lr;    // of the unit
+            const bool live = row < s.rows;
+            // a warp without live rows leaves P as it is: it only reaches its own rows of O
+            const bool idle = dual ? T * h + 32 * (warp & 3) >= s.rows : ((32 * (warp & 3)) & (rows_per - 1)) >= s.rows;
+            const int nd = live ? (int)p.fd_g.div((uint32_t)(gr0 + row)) : 0;
+            const float cs = sm.cs[dual ? h : 0][r];
+            const int c_lo = part << (2 - lg_parts), c_hi = c_lo + (4 >> lg_parts);   // 32-token chunks
+            float m_run = -INFINITY, l_run = 0.0f;
+            float m_sum = -INFINITY;                  // m of the flushed O
+            int own = 0;                              // this group's items of the segment so far
+#pragma unroll 1
+            for (int i = (int)((gi ^ h) & 1); i < s.tiles << dual; i += 2, ++own) {
+                const uint32_t x = gi + i;
+                const int t0 = (s.tile0 + (i >> dual)) * T;
+                wait_warp(&sm.sready[h], (x >> 1) & 1, abort_flag, p.status, polls);
+                tc::fence_after_sync();
+                if (!idle) {
+                    const bool tail = t0 + T > s.start;
+                    // ---- the row's max over its tokens ----
+                    uint32_t v[32];
+                    float mt = -INFINITY;
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; ++c) {
+                        tc::tmem_ld_x16(scol + 32 * c, v);
+                        tc::tmem_ld_x16(scol + 32 * c + 16, v + 16);
                         tc::tmem_wait_ld();
-                        if (t0 + T > s.start) {
-                            const uint64_t vis = visible64(p, s, node[rb], t0 + 64 * h);
+                        if (tail) {
+                            const uint32_t vis = (uint32_t)visible64(p, s, nd, t0 + 32 * c);
 #pragma unroll
-                            for (int j = 0; j < 64; ++j)
+                            for (int j = 0; j < 32; ++j)
                                 if (!((vis >> j) & 1)) v[j] = 0xFF800000u;
                         }
-                        float mt = __uint_as_float(v[0]);
+                        float m4[4] = {__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
 #pragma unroll
-                        for (int j = 1; j < 64; ++j) mt = fmaxf(mt, __uint_as_float(v[j]));
-                        mt *= cs[rb];
-                        sm.mx[sb][h][r] = mt;
-                        ok = pair_and(bar, ok);
-                        if (!ok) break;
-                        mt = fmaxf(mt, sm.mx[sb][h ^ 1][r]);
-                        float m_new = m_run[rb];
-                        if (mt > m_new + kSlack || m_new == -INFINITY) m_new = fmaxf(m_new, mt);
-                        float f = 1.0f;
-                        if (m_new != m_run[rb]) {
-                            f = m_run[rb] == -INFINITY ? 0.0f : fast_exp2(m_run[rb] - m_new);
-                            l_run[rb] *= f;
-                            m_run[rb] = m_new;
-                        }
-                        // tcgen05.ld/st are warp-wide: the warp rescales when any of its rows must
-                        const bool flush = TWO && k > 0 && k % kFlush == 0;
-                        if (k > 0 && (flush || __any_sync(0xFFFFFFFFu, f != 1.0f))) {
-                            // P . V of this row block's previous tile has ended (with two row
-                            // blocks it was issued before this S, so it has)
-                            const uint32_t pt = gt + k - 1;
-                            if (nrb == 1) ok = wait_warp(&sm.vfree[pt & 1], (pt >> 1) & 1, abort_flag, p.status, polls);
-                            tc::fence_after_sync();
+                        for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[j]));
+                        mt = fmaxf(mt, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    }
+                    mt *= cs;
+                    float f = 1.0f;
+                    if (mt > m_run + kSlack || m_run == -INFINITY) {
+                        const float m_new = fmaxf(m_run, mt);
+                        f = m_new == m_run ? 1.0f : (m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_new));
+                        l_run *= f;
+                        m_run = m_new;
+                    }
+                    // The group's O is complete: its last P . V was issued before this S.
+                    // (tcgen05.ld/st are warp-wide: all rows rescale when any must.)
+                    const bool flush = TWO && own > 0 && own % kFlush == 0;
+                    if (own > 0 && (flush || __any_sync(0xFFFFFFFFu, f != 1.0f))) {
+                        const float fs = m_sum == -INFINITY ? 0.0f : fast_exp2(m_sum - m_run);
 #pragma unroll 1
-                            for (int c = 0; c < DH / 16; ++c) {
-                                uint32_t o[16];
-                                const uint32_t col = DH * h + 16 * c;
-                                const uint32_t oc = trow + C::kColO + D * rb + col, mc = trow + C::kColM + col;
-                                tc::tmem_ld_x16(oc, o);
-                                tc::tmem_wait_ld();
-                                if (TWO && k > kFlush) {
-                                    uint32_t m[16];
-                                    tc::tmem_ld_x16(mc, m);
-                                    tc::tmem_wait_ld();
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc::tmem_ld_x16(ocol + c, o);
+                            tc::tmem_wait_ld();
+                            if (flush) {
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j)
-                                        m[j] = __float_as_uint(
-                                            (__uint_as_float(m[j]) + (flush ? __uint_as_float(o[j]) : 0.0f)) * f);
-                                    tc::tmem_st_x8(mc, m);
-                                    tc::tmem_st_x8(mc + 8, m + 8);
+                                for (int j = 0; j < 16; ++j) {
+                                    float y = __uint_as_float(o[j]) * f;
+                                    if (own > kFlush) y = __fmaf_rn(sums[(c + j) * T], fs, y);
+                                    sums[(c + j) * T] = y;
                                 }
+                            } else {
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                if (!flush) {
-                                    tc::tmem_st_x8(oc, o);
-                                    tc::tmem_st_x8(oc + 8, o + 8);
-                                } else if (k == kFlush) {
-                                    tc::tmem_st_x8(mc, o);
-                                    tc::tmem_st_x8(mc + 8, o + 8);
-                                }
+                                tc::tmem_st_x8(ocol + c, o);
+                                tc::tmem_st_x8(ocol + c + 8, o + 8);
                             }
                         }
-                        const float base = (m_run[rb] == -INFINITY ? 0.0f : m_run[rb]) - kBias;
-                        uint32_t ph[32];
-                        float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float a = fast_exp2(__fmaf_rn(__uint_as_float(v[2 * j]), cs[rb], -base));
-                            const float b = fast_exp2(__fmaf_rn(__uint_as_float(v[2 * j + 1]), cs[rb], -base));
-                            sum0 += a;
-                            sum1 += b;
-                            ph[j] = pack_f16x2(a, b);
-                            if (TWO) v[j] = pack_f16x2(a - f16_lo_to_float(ph[j]), b - f16_hi_to_float(ph[j]));
-                        }
-                        l_run[rb] += sum0 + sum1;
-                        tc::tmem_st_x32(scol, ph);
-                        if (TWO) {
-                            uint32_t pl[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) pl[j] = v[j];
-                            tc::tmem_st_x32(scol + 32, pl);
-                        }
-                        tc::tmem_wait_st();
+                        if (flush) m_sum = m_run;
                     }
-                    tc::fence_before_sync();
-                    mbar_arrive(&sm.pready[sb]);
-                    ++gi;
+                    // ---- weights: chunk c to columns 32c .. 32c + 15 (second terms: + 16) ----
+                    const float base = (m_run == -INFINITY ? 0.0f : m_run) - kBias;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; ++c) {
+                        if (lg_parts < 2) {           // else the one chunk is still here
+                            tc::tmem_ld_x16(scol + 32 * c, v);
+                            tc::tmem_ld_x16(scol + 32 * c + 16, v + 16);
+                            tc::tmem_wait_ld();
+                            if (tail) {
+                                const uint32_t vis = (uint32_t)visible64(p, s, nd, t0 + 32 * c);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (!((vis >> j) & 1)) v[j] = 0xFF800000u;
+                            }
+                        }
+                        uint32_t lo16[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float a = fast_exp2(__fmaf_rn(__uint_as_float(v[2 * j]), cs, -base));
+                            const float b = fast_exp2(__fmaf_rn(__uint_as_float(v[2 * j + 1]), cs, -base));
+                            sum[2 * (j & 1)] += a;
+                            sum[2 * (j & 1) + 1] += b;
+                            v[j] = pack_f16x2(a, b);
+                            if (TWO) lo16[j] = pack_f16x2(a - f16_lo_to_float(v[j]), b - f16_hi_to_float(v[j]));
+                        }
+                        tmem_st_x16(scol + 32 * c, v);
+                        if (TWO) tmem_st_x16(scol + 32 * c + 16, lo16);
+                    }
+                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc::tmem_wait_st();
                 }
+                tc::fence_before_sync();
+                bar_tell(kBarP + h, 160, abort_flag);
             }
-            gt += s.tiles;
-            // ---- the segment's O: the output when it is a whole unit, else a partial ----
-            const uint32_t last = gt - 1;
-            ok = ok && wait_warp(&sm.vfree[last & 1], (last >> 1) & 1, abort_flag, p.status, polls);
-            if (32 * (warp & 3) < s.rows) ok = pair_and(bar, ok);
-            if (!ok) break;
+            gi += (uint32_t)s.tiles << dual;
+
+            // ---- both groups' O are complete: their shares of a row ----
+            // (the last two items' P . V: one of each group, or there was one item)
+            for (uint32_t x = gi >= 2 ? gi - 2 : 0; x < gi; ++x)
+                wait_warp(&sm.pdone[x & 1], (x >> 1) & 1, abort_flag, p.status, polls);
+            sm.ml[h][0][r] = live ? m_run : -INFINITY;
+            sm.ml[h][1][r] = live ? l_run : 0.0f;
+            softmax_sync();
             tc::fence_after_sync();
             const bool whole = s.tiles == s.unit_tiles;
             float* const slot = p.partials + (int64_t)(2 * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * C::kSlot;
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                if (rb >= nrb || rb * T + 32 * (warp & 3) >= s.rows) continue;
-                const int row = rb * T + r;
-                const bool live = row < s.rows;
-                sm.mx[rb][h][r] = l_run[rb];
-                pair_and(bar, true);
-                const float l = l_run[rb] + sm.mx[rb][h ^ 1][r];
-                pair_and(bar, true);                  // the exchange is read before the next one writes
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                const int gr = s.ru * RB * T + row;
-                const int64_t orow =
-                    (((int64_t)s.b * p.N + node[rb]) * p.Hq + (int64_t)s.hk * p.g + (gr - node[rb] * p.g)) * D + DH * h;
-#pragma unroll 1
-                for (int c = 0; c < DH / 16; ++c) {
-                    uint32_t o[16];
-                    tc::tmem_ld_x16(trow + C::kColO + D * rb + DH * h + 16 * c, o);
-                    tc::tmem_wait_ld();
-                    if (TWO && s.tiles > kFlush) {
-                        uint32_t m[16];
-                        tc::tmem_ld_x16(trow + C::kColM + DH * h + 16 * c, m);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) + __uint_as_float(m[j]));
-                    }
-                    if (!live) continue;
-                    if (!whole) {
-                        float4* dst = reinterpret_cast<float4*>(slot + (int64_t)row * D + DH * h + 16 * c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                 __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
-                    } else if (TWO) {
-                        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + orow + 16 * c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
-                                                 __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + 16 * c);
-                        uint32_t x[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv,
-                                                                           __uint_as_float(o[2 * j + 1]) * inv);
-                            x[j] = *reinterpret_cast<const uint32_t*>(&y);
-                        }
-                        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-                        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
-                    }
+            // m and l of the row over its copies and, unless each group has its own rows, groups
+            float m_all = -INFINITY, l_all = 0.0f;
+            for (int g = dual ? h : 0; g < (dual ? h + 1 : 2); ++g)
+                for (int q = 0; q < 1 << lg_parts; ++q) m_all = fmaxf(m_all, sm.ml[g][0][lr + q * rows_per]);
+            for (int g = dual ? h : 0; g < (dual ? h + 1 : 2); ++g)
+                for (int q = 0; q < 1 << lg_parts; ++q) {
+                    const float mq = sm.ml[g][0][lr + q * rows_per];
+                    l_all += mq == -INFINITY ? 0.0f : sm.ml[g][1][lr + q * rows_per] * fast_exp2(mq - m_all);
                 }
-                if (!whole && live && h == 0) {
-                    slot[(int64_t)RB * T * D + row] = m_run[rb];
-                    slot[(int64_t)RB * T * (D + 1) + row] = l;
+            const float inv = whole ? (l_all > 0.0f ? 1.0f / l_all : 0.0f) : 1.0f;
+            // factors of the groups' O (of this copy); 0 where a group saw nothing: O is anything then
+            float fo[2], ff[2];                       // of O, and of what was flushed of it
+            int flushed[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float mg = dual && g != h ? -INFINITY : sm.ml[g][0][r];
+                fo[g] = mg == -INFINITY ? 0.0f : fast_exp2(mg - m_all) * inv;
+                ff[g] = 0.0f;
+                flushed[g] = 0;
+            }
+            if (TWO) {
+                // the groups exchange the m of their flushed sums
+                const int mine = own > 0 ? (own - 1) / kFlush : 0;
+                softmax_sync();
+                sm.ml[h][0][r] = mine > 0 ? m_sum : -INFINITY;
+                softmax_sync();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float mg = dual && g != h ? -INFINITY : sm.ml[g][0][r];
+                    ff[g] = mg == -INFINITY ? 0.0f : fast_exp2(mg - m_all) * inv;
+                    flushed[g] = !dual || g == h;
                 }
             }
+            const int64_t at =
+                (((int64_t)s.b * p.N + nd) * p.Hq + (int64_t)s.hk * p.g + (gr0 + row - nd * p.g)) * D;
+            // Columns 16 at a time: group h takes every other 16 (all of them when the rows
+            // are its own).  The copies' sums meet in the query buffer, [copy][column][row].
+            // (Two buffers where the query buffer holds them: one barrier less.)
+            constexpr bool TWOBUF = sizeof(sm.q[0]) >= 4 * T * 16 * sizeof(float);
+            float* const meet0 = reinterpret_cast<float*>(sm.q[0]) + h * (T * 16);
+#pragma unroll 1
+            for (int c = dual ? 0 : 16 * h; c < D; c += dual ? 16 : 32) {
+                float y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = 0.0f;
+                if (!idle) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (dual && g != h) continue;
+                        uint32_t o[16];
+                        tc::tmem_ld_x16(trow + C::kColO + D * g + c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (fo[g] != 0.0f) y[j] = __fmaf_rn(__uint_as_float(o[j]), fo[g], y[j]);
+                            if (TWO && flushed[g] && ff[g] != 0.0f)
+                                y[j] = __fmaf_rn(p.sums[((int64_t)(2 * blockIdx.x + g) * D + c + j) * T + r], ff[g], y[j]);
+                        }
+                    }
+                }
+                if (lg_parts > 0) {
+                    float* const meet = meet0 + (TWOBUF && (c & 32) ? 2 * T * 16 : 0);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) meet[j * T + r] = y[j];
+                    bar_sync(kBarMeet + h, 128);
+                    if (part == 0 && live)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            y[j] += meet[j * T + lr + rows_per];
+                            if (lg_parts == 2) y[j] += meet[j * T + lr + 64] + meet[j * T + lr + 96];
+                        }
+                    if (!TWOBUF) bar_sync(kBarMeet + h, 128);   // read before it is written again
+                }
+                if (!live || part > 0) continue;
+                if (!whole) {
+                    float4* dst = reinterpret_cast<float4*>(slot) + (c / 4) * (RB * T) + row;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j * (RB * T)] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                } else if (TWO) {
+                    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at + c);
+                    uint32_t x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+                        x[j] = *reinterpret_cast<const uint32_t*>(&z);
+                    }
+                    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+                }
+            }
+            if (!whole && live && part == 0 && (dual || h == 0)) {
+                reinterpret_cast<float2*>(slot + (int64_t)RB * T * D)[row] = make_float2(m_all, l_all);
+            }
             tc::fence_before_sync();
-            mbar_arrive(&sm.oread);
+            softmax_sync();                           // O, the query buffer and the exchanges have been read
+            if (tid == 0) mbar_arrive(&sm.oread);
         }
     }
 
@@ -763,31 +886,41 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     constexpr int RPB = kMergeThreads / (D / 4);      // rows of a block
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = p.desc[blockIdx.x];
-    if (d.x == 0) return;
-    int err;
-    const int nodes = live_nodes(p, d.y, p.start[d.y], err);
-    const int gr0 = d.w * RB * T;
-    const int row = blockIdx.y * RPB + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
-    if (row >= min(RB * T, nodes * p.g - gr0)) return;
+    const int parts = d.x & 0xFFFF, rows = d.x >> 16, gr0 = d.w * RB * T;
+    const int row = blockIdx.y * RPB + threadIdx.x % RPB, col = 4 * (threadIdx.x / RPB);
+    if (row >= rows) return;
     const int c0 = (int)blockIdx.x - 1;
-    auto slot = [&](int j) -> const float* { return p.partials + (int64_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlot; };
-    float M = -INFINITY;
-    for (int j = 0; j < d.x; ++j) M = fmaxf(M, __ldcg(slot(j) + RB * T * D + row));
-    float L = 0.0f;
+    float M = -INFINITY, L = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int j = 0; j < d.x; ++j) {
-        const float* sp = slot(j);
-        const float m = __ldcg(sp + RB * T * D + row);
-        const float w = m == -INFINITY ? 0.0f : fast_exp2(m - M);
-        const float l = __ldcg(sp + RB * T * (D + 1) + row);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(sp + (int64_t)row * D + col));
-        if (w > 0.0f) {                               // a contributor that saw nothing left its O undefined
-            L = __fmaf_rn(l, w, L);
-            acc.x = __fmaf_rn(o.x, w, acc.x);
-            acc.y = __fmaf_rn(o.y, w, acc.y);
-            acc.z = __fmaf_rn(o.z, w, acc.z);
-            acc.w = __fmaf_rn(o.w, w, acc.w);
+    // four contributors' loads in flight, joined under a running maximum
+#pragma unroll 1
+    for (int j0 = 0; j0 < parts; j0 += 4) {
+        float2 ml[4];
+        float4 o[4];
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = min(j0 + k, parts - 1);
+            const float* sp = p.partials + (int64_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * kSlot;
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(sp + RB * T * D) + row);
+            o[k] = __ldcg(reinterpret_cast<const float4*>(sp) + (col / 4) * (RB * T) + row);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) Mn = fmaxf(Mn, ml[k].x);
+        const float f = M == -INFINITY ? 0.0f : fast_exp2(M - Mn);
+        L *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+        M = Mn;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // a contributor that saw nothing left its O undefined
+            const float w = j0 + k >= parts || ml[k].x == -INFINITY ? 0.0f : fast_exp2(ml[k].x - M);
+            if (w > 0.0f) {
+                L = __fmaf_rn(ml[k].y, w, L);
+                acc.x = __fmaf_rn(o[k].x, w, acc.x);
+                acc.y = __fmaf_rn(o[k].y, w, acc.y);
+                acc.z = __fmaf_rn(o[k].z, w, acc.z);
+                acc.w = __fmaf_rn(o[k].w, w, acc.w);
+            }
         }
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
@@ -813,11 +946,13 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
     cudaError_t e =
         ensure_smem_attribute(reinterpret_cast<const void*>(tree_attention_tc_kernel<C, TWO>), smem, configured);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<C, TWO><<<(unsigned)grid, kThreads, smem, stream>>>(p);
+    tree_attention_tc_kernel<C, TWO><<<(unsigned)grid, C::kThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(C::RB * T / (kMergeThreads / (C::D / 4))));
+    const int most_rows = (int)std::min<int64_t>((int64_t)p.N * p.g, C::RB * T);
+    constexpr int kRows = kMergeThreads / (C::D / 4);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)((most_rows + kRows - 1) / kRows));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -828,18 +963,19 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<C::D, C::RB>, p);
 }
 
-// Row blocks of a unit: two when some sequence can have more than 128 rows and
-// the output is bf16 (with fp32 outputs the second accumulator takes the tensor
-// memory of the second row block).
-int row_blocks(int N, int g, bool out_bf16) { return out_bf16 && (int64_t)N * g > T ? 2 : 1; }
+// row blocks of a unit: two when some sequence can have more than 128 rows
+int row_blocks(int N, int g) { return (int64_t)N * g > T ? 2 : 1; }
+
+size_t desc_bytes(size_t sms) { return (sms * sizeof(int4) + 255) / 256 * 256; }
+size_t partial_bytes(size_t sms, int rb, int D) { return 2 * sms * (size_t)rb * T * (D + 2) * sizeof(float); }
 
 }  // namespace
 
 size_t tree_attention_workspace(int B, int N, int Hq, int Hkv, int D) {
     (void)B;
     const size_t sms = (size_t)device_sm_count();
-    const size_t slot = (size_t)row_blocks(N, Hq / Hkv, true) * T * (D + 2) * sizeof(float);
-    return ((sms * sizeof(int4) + 255) / 256 * 256) + 2 * sms * slot;
+    // units cut by the ranges, their partials, and the flushed sums of fp32 outputs
+    return desc_bytes(sms) + partial_bytes(sms, row_blocks(N, Hq / Hkv), D) + 2 * sms * (size_t)T * D * sizeof(float);
 }
 
 cudaError_t launch_tree_attention(const TreeLaunch& a, cudaStream_t stream) {
@@ -847,9 +983,11 @@ cudaError_t launch_tree_attention(const TreeLaunch& a, cudaStream_t stream) {
     const int sms = device_sm_count();
     p.st_k = a.st_k; p.st_v = a.st_v;
     p.mask_stride = a.mask_stride;
-    p.desc = reinterpret_cast<int4*>(a.partials);
-    p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partials) +
-                                          (((size_t)sms * sizeof(int4) + 255) / 256 * 256));
+    const int rb = row_blocks(a.N, a.Hq / a.Hkv);
+    uint8_t* const ws = reinterpret_cast<uint8_t*>(a.partials);
+    p.desc = reinterpret_cast<int4*>(ws);
+    p.partials = reinterpret_cast<float*>(ws + desc_bytes(sms));
+    p.sums = reinterpret_cast<float*>(ws + desc_bytes(sms) + partial_bytes(sms, rb, a.D));
     p.status = a.status;
     p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.g = a.Hq / a.Hkv; p.S_max = a.S_max;
     p.W = (a.N + 31) / 32;
@@ -859,7 +997,6 @@ cudaError_t launch_tree_attention(const TreeLaunch& a, cudaStream_t stream) {
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_polls = a.wait_polls;
     p.fd_g = FastDiv((uint32_t)p.g);
-    const int rb = row_blocks(a.N, p.g, a.out_bf16);
     for (int b0 = 0; b0 < a.B; b0 += kMaxBatchPerLaunch) {
         p.B = a.B - b0 < kMaxBatchPerLaunch ? a.B - b0 : kMaxBatchPerLaunch;
         p.q = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)b0 * a.N * a.Hq * a.D;
@@ -877,11 +1014,11 @@ cudaError_t launch_tree_attention(const TreeLaunch& a, cudaStream_t stream) {
         const int grid = (int)(most < sms ? most : sms);
         cudaError_t e;
         if (a.D == 128)
-            e = !a.out_bf16 ? launch<Cfg<128, 1>, true>(p, grid, stream)
-                            : (rb == 2 ? launch<Cfg<128, 2>, false>(p, grid, stream) : launch<Cfg<128, 1>, false>(p, grid, stream));
+            e = rb == 2 ? (a.out_bf16 ? launch<Cfg<128, 2>, false>(p, grid, stream) : launch<Cfg<128, 2>, true>(p, grid, stream))
+                        : (a.out_bf16 ? launch<Cfg<128, 1>, false>(p, grid, stream) : launch<Cfg<128, 1>, true>(p, grid, stream));
         else
-            e = !a.out_bf16 ? launch<Cfg<64, 1>, true>(p, grid, stream)
-                            : (rb == 2 ? launch<Cfg<64, 2>, false>(p, grid, stream) : launch<Cfg<64, 1>, false>(p, grid, stream));
+            e = rb == 2 ? (a.out_bf16 ? launch<Cfg<64, 2>, false>(p, grid, stream) : launch<Cfg<64, 2>, true>(p, grid, stream))
+                        : (a.out_bf16 ? launch<Cfg<64, 1>, false>(p, grid, stream) : launch<Cfg<64, 1>, true>(p, grid, stream));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
