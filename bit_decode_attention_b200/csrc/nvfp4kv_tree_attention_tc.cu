@@ -46,9 +46,9 @@
 // Measured (B200, head_dim 128; a tile's raw bytes take 774 clocks of an SM's share
 // of 6.55 TB/s, its MMAs 512 with one row block and 1,024 with two):
 //   128 sequences x 8 KV heads, up to 8 nodes x 4 heads, 1,024 to 8,192 tokens:
-//     374 us, 2,140 clocks a tile; a loop of named waits paces it: dequant 2,300 to 2,900 (the SM issues
-//     0.59 instructions a clock and scheduler, the integer pipe is 58% busy), MMA
-//     issue and completion 1,000 until the buffer is free again, two buffers
+//     374 us, 2,140 clocks a tile.  A loop of waits paces it, for each of two buffers:
+//     dequant 2,300 to 2,900 (the SM issues 0.59 instructions a clock and scheduler,
+//     the integer pipe is 58% busy), then 1,000 of MMA issue and completion
 //   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 102 us, 4,700 clocks
 //     a tile; the softmax paces it: 3,300 of arithmetic (256 x 128 exponentials are
 //     2,048 at the SM's 16 a clock) and 1,400 between P and the next scores

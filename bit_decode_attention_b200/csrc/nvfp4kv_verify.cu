@@ -16,8 +16,15 @@
 // pass over the vocabulary, of which each CTA takes a slice and each warp a
 // contiguous chunk.  The chunks' sums are kept, so that the last pass also
 // says which warp's chunk holds the sampled token; that warp alone reads its
-// chunk again (from L2).  Bound by HBM for large batches, by the chain of
-// memory latencies and cluster barriers for one sequence.
+// chunk again (from L2).
+//
+// Measured (B200): one sequence, 6 nodes over 32,000 tokens: 8.4 us, a chain of
+// memory latencies and cluster barriers.  64 sequences, up to 16 nodes over
+// 131,072: 41 us, where 59 MB of rows take 9 at 6.55 TB/s: a sequence waits for
+// two or three passes in turn, of 10 us each; 12 of the 41 are the 64-bit weights
+// (conversions run at 16 a clock and SM).  Loops over elements unrolled further,
+// or the loop over rejections inside them, make the code larger than the
+// instruction cache holds: 72 us and 18.5.
 #include <cooperative_groups.h>
 
 #include "nvfp4kv_device.cuh"
@@ -29,8 +36,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+// Of 4 CTAs an SM.  512 threads (2 an SM): 42 us as here for 64 sequences of 16 nodes
+// over 131,072 tokens, 10.3 for 8.4 for one of 6 over 32,000, 26 for 16 for 64 of
+// those, but 12.4 for 15.0 for one over 131,072.
+constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 
 struct VerifyParams {
     const void* p;                                    // [B][N][V]
@@ -73,62 +82,86 @@ __device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&v)
     }
 }
 
+// 16-byte aligned, a multiple of 16 bytes
+__device__ __forceinline__ void prefetch_l2(const void* from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
 // NaN and negative weights count as 0
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 struct Shared {
     double z[kTreeMaxNodes];                          // Z subtracted by each rejection of the current node
     float pp[kTreeMaxNodes], dd[kTreeMaxNodes];       // p and d of a node's token at its parent
     float ua[kTreeMaxNodes];
     int32_t token[kTreeMaxNodes], parent[kTreeMaxNodes];
-    int32_t rejected[kTreeMaxNodes];                  // the rejected nodes of the current node
+    int32_t rejected[kTreeMaxNodes];                  // the tokens of the current node's rejections
     double warp_sum[kWarps];
-    double total[2];                                  // this CTA's slice sum, two passes' worth
+    double total[2][kCluster];                        // the CTAs' sums of the last two passes
 };
 
-template <bool F32, int VEC>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyParams q) {
+// DRAFT: with the draft's distribution; else point masses
+template <bool F32, int VEC, bool DRAFT>
+__global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const VerifyParams q) {
     __shared__ Shared sm;
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), nranks = (int)cluster.num_blocks();
+    cluster_arrive();
+    const int rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = (int)(blockIdx.x / (unsigned)nranks);
+    const int b = (int)(blockIdx.x / (unsigned)kCluster);
     const int N = q.N, V = q.V;
+    const int64_t row0 = (int64_t)b * N;
     const int n = q.n_nodes != nullptr ? q.n_nodes[b] : N;
+    const float us = q.u_sample[b];
+
+    // the tested tokens' probabilities; a node with a bad parent or token is never tested
+#pragma unroll 1
+    for (int i = tid; i < N; i += kThreads) {
+        const int32_t par = q.parents[(int64_t)b * q.parent_stride + i];
+        const int32_t tok = q.tokens[row0 + i];
+        const float ua = q.u_accept[row0 + i];
+        const bool ok = i > 0 && par >= 0 && par < i && tok >= 0 && tok < V;
+        if (i > 0 && i < n && n <= N && !ok && rank == 0) report(q.status, NVFP4_ERR_INVALID_ARG);
+        sm.parent[i] = ok ? par : -1;
+        sm.token[i] = tok;
+        sm.ua[i] = ua;
+        sm.pp[i] = ok && i < n ? load1<F32>(q.p, (row0 + par) * V + tok) : 0.0f;
+        sm.dd[i] = DRAFT && ok && i < n ? load1<F32>(q.d, (row0 + par) * V + tok) : 1.0f;
+    }
     if (n < 1 || n > N) {                             // 0: a padding row, left as it was
         if (n != 0 && rank == 0 && tid == 0) report(q.status, NVFP4_ERR_INVALID_ARG);
         return;                                       // the whole cluster
     }
-    const int64_t row0 = (int64_t)b * N;
-
-    // the tested tokens' probabilities; a node with a bad parent or token is never tested
-    for (int i = tid; i < n; i += kThreads) {
-        const int32_t par = q.parents[(int64_t)b * q.parent_stride + i];
-        const int32_t tok = q.tokens[row0 + i];
-        const bool ok = i > 0 && par >= 0 && par < i && tok >= 0 && tok < V;
-        if (i > 0 && !ok && rank == 0) report(q.status, NVFP4_ERR_INVALID_ARG);
-        sm.parent[i] = ok ? par : -1;
-        sm.token[i] = tok;
-        sm.ua[i] = q.u_accept[row0 + i];
-        sm.pp[i] = ok ? load1<F32>(q.p, (row0 + par) * V + tok) : 0.0f;
-        sm.dd[i] = ok && q.d != nullptr ? load1<F32>(q.d, (row0 + par) * V + tok) : 1.0f;
-    }
     __syncthreads();
+    cluster_wait();                                   // every CTA has started: its memory may be written
 
     int at = 0, nrej = 0, passes = 0, n_acc = 1;
     double Z = 1.0;
     bool sums_valid = false;                          // warp_sum and total hold the current weights' sums
 
-    // w of token x (probability pv, draft dv) after the first k rejections
-    auto weight = [&](float pv, double dv, int x, int k) -> double {
-        double w = (double)fmaxf(pv, 0.0f);           // NaN gives 0
-        if (q.d != nullptr) {
-            for (int j = 0; j < k; ++j) w = positive(w - sm.z[j] * dv);
-        } else {
-            for (int j = 0; j < k; ++j)
-                if (sm.token[sm.rejected[j]] == x) w = positive(w - sm.z[j]);
+    // E weights at once, of tokens x, x + 1, .. (probability pv, draft dv), after the
+    // first k rejections.  NaN counts as 0.  (The loop over rejections stays rolled:
+    // unrolled over elements too, the code would be the kernel's time.)
+    auto weights = [&](auto& w, const auto& pv, const auto& dv, int x, int k) {
+        constexpr int E = (int)(sizeof(pv) / sizeof(float));
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = (double)fmaxf(pv[e], 0.0f);
+#pragma unroll 1
+        for (int j = 0; j < k; ++j) {
+            const double z = sm.z[j];
+            if (DRAFT) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) w[e] = positive(w[e] - z * (double)dv[e]);
+            } else {
+                const uint32_t at_e = (uint32_t)(sm.rejected[j] - x);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (at_e == (uint32_t)e) w[e] = positive(w[e] - z);
+            }
         }
-        return w;
     };
     const int slice = q.chunk * kWarps;
     const int64_t lo = (int64_t)rank * slice + (int64_t)warp * q.chunk;
@@ -136,51 +169,64 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
     // sum of the weights after k rejections of node `at`, over the cluster
     auto pass = [&](int k) -> double {
         const int64_t base = (row0 + at) * V;
-        const bool use_d = q.d != nullptr && k > 0;
         double s = 0.0;
-        constexpr int U = 4;
+        if (VEC > 1 && lane == 0 && lo < hi) {        // the chunk to L2 at once: its loads then wait for no DRAM
+            constexpr int ES = F32 ? 4 : 2;
+            const uint32_t bytes = (uint32_t)(hi - lo) * ES;
+            prefetch_l2(static_cast<const uint8_t*>(q.p) + (base + lo) * ES, bytes);
+            if (DRAFT && k > 0) prefetch_l2(static_cast<const uint8_t*>(q.d) + (base + lo) * ES, bytes);
+        }
+        constexpr int U = VEC == 8 ? 1 : 2;          // loads of each row in flight
+#pragma unroll 1
         for (int64_t i0 = lo + lane * VEC; i0 < hi; i0 += 32 * VEC * U) {
             float pv[U][VEC], dv[U][VEC];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t i = i0 + u * 32 * VEC;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) pv[u][e] = dv[u][e] = 0.0f;
                 if (i < hi) {
                     load_vec<F32, VEC>(q.p, base + i, pv[u]);
-                    if (use_d) load_vec<F32, VEC>(q.d, base + i, dv[u]);
+                    if (DRAFT && k > 0) load_vec<F32, VEC>(q.d, base + i, dv[u]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t i = i0 + u * 32 * VEC;
-                if (i < hi) {
+                double w[VEC];
+                weights(w, pv[u], dv[u], (int)(i0 + u * 32 * VEC), k);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        s += weight(pv[u][e], use_d ? (double)dv[u][e] : 0.0, (int)i + e, k);
-                }
+                for (int e = 0; e < VEC; ++e) s += w[e];
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (lane == 0) sm.warp_sum[warp] = s;
         __syncthreads();
-        double* slot = &sm.total[passes & 1];
-        if (tid == 0) {
-            double t = 0.0;
-            for (int w = 0; w < kWarps; ++w) t += sm.warp_sum[w];
-            *slot = t;
+        // Every CTA gives its sum to all of them.  (The slot's last readers came to the
+        // barrier of the pass between.)
+        double* const slot = sm.total[passes & 1];
+        if (warp == 0) {
+            double t = lane < kWarps ? sm.warp_sum[lane] : 0.0;
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+            if (lane < kCluster) *cluster.map_shared_rank(slot + rank, lane) = t;
         }
         cluster.sync();
         double t = 0.0;
-        for (int r = 0; r < nranks; ++r) t += *cluster.map_shared_rank(slot, r);
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) t += slot[r];
         ++passes;
         return t;
     };
 
     if (rank == 0 && tid == 0) q.path[row0] = 0;
+#pragma unroll 1
     for (int i = 1; i < n; ++i) {
         if (sm.parent[i] != at) continue;             // uniform over the cluster
-        const double w = weight(sm.pp[i], (double)sm.dd[i], sm.token[i], nrej);
-        if ((double)sm.ua[i] * (double)sm.dd[i] * Z < w) {
+        const float pv[1] = {sm.pp[i]}, dv[1] = {sm.dd[i]};
+        double w[1];
+        weights(w, pv, dv, sm.token[i], nrej);
+        if ((double)sm.ua[i] * (double)dv[0] * Z < w[0]) {
             if (rank == 0 && tid == 0) q.path[row0 + n_acc] = i;
             ++n_acc;
             at = i;
@@ -192,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
         __syncthreads();                              // readers of the previous list are done
         if (tid == 0) {
             sm.z[nrej] = Z;
-            sm.rejected[nrej] = i;
+            sm.rejected[nrej] = sm.token[i];
         }
         __syncthreads();
         const double total = pass(nrej + 1);
@@ -215,12 +261,12 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
         // the slice, then the warp's chunk, then the 1/16 of that chunk, then the
         // element whose inclusive sum is the first past the target; should
         // rounding pass the end, the last one that holds any weight
-        const float us = q.u_sample[b];
         const double target = us > 0.0f ? (double)us * total : 0.0;
         double before = 0.0, mine = 0.0;
         bool last = true;
-        for (int r = 0; r < nranks; ++r) {
-            const double t = *cluster.map_shared_rank(&sm.total[(passes - 1) & 1], r);
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+            const double t = sm.total[(passes - 1) & 1][r];
             if (r < rank) before += t;
             if (r == rank) mine = t;
             if (r > rank && t > 0.0) last = false;
@@ -230,6 +276,7 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             auto first_past = [&](double& acc) -> int {
                 int hit = 0;
                 double at_hit = acc;
+#pragma unroll 1
                 for (int w = 0; w < kWarps; ++w) {
                     const double s = sm.warp_sum[w];
                     if (s > 0.0) {
@@ -245,17 +292,21 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             double acc = before;
             const int hit = first_past(acc);
             const int64_t base = (row0 + at) * V;
-            const int sub = q.chunk / kWarps;         // a multiple of 32
+            const int sub = q.chunk / kWarps;          // a multiple of 32
             const int64_t s0 = (int64_t)rank * slice + (int64_t)hit * q.chunk + (int64_t)warp * sub;
             const int64_t s1 = s0 + sub < V ? s0 + sub : V;
             auto weight_at = [&](int64_t i) -> double {
-                return i < s1 ? weight(load1<F32>(q.p, base + i),
-                                       q.d != nullptr && nrej > 0 ? (double)load1<F32>(q.d, base + i) : 0.0, (int)i,
-                                       nrej)
-                              : 0.0;
+                float pv[1] = {0.0f}, dv[1] = {0.0f};
+                if (i < s1) {
+                    pv[0] = load1<F32>(q.p, base + i);
+                    if (DRAFT && nrej > 0) dv[0] = load1<F32>(q.d, base + i);
+                }
+                double w[1];
+                weights(w, pv, dv, (int)i, nrej);
+                return w[0];
             };
             double s = 0.0;
-#pragma unroll 4
+#pragma unroll 1
             for (int64_t i0 = s0; i0 < s1; i0 += 32) s += weight_at(i0 + lane);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -264,6 +315,7 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             __syncthreads();
             if (warp == first_past(acc)) {
                 int answer = -1, best = 0;
+#pragma unroll 1
                 for (int64_t i0 = s0; i0 < s1 && answer < 0; i0 += 32) {
                     const double w = weight_at(i0 + lane);
                     double c = w;
@@ -282,23 +334,31 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             }
         }
     }
-    cluster.sync();                                   // no CTA leaves while others read its sums
+    // (After the last pass's barrier no CTA touches another's memory.)
 }
 
-template <bool F32, int VEC>
-cudaError_t launch(const VerifyParams& q, int B, int cluster, cudaStream_t stream) {
+template <bool F32, int VEC, bool DRAFT>
+cudaError_t launch(VerifyParams& q, int B, cudaStream_t stream) {
+    constexpr int align = 32 * kWarps;                 // whole 32-element rows for each warp's share of a chunk
+    const int64_t chunk = ((int64_t)q.V + kCluster * kWarps - 1) / (kCluster * kWarps);
+    q.chunk = (int32_t)((chunk + align - 1) / align * align);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(B * cluster));
+    cfg.gridDim = dim3((unsigned)(B * kCluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.x = (unsigned)kCluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<F32, VEC>, q);
+    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<F32, VEC, DRAFT>, q);
+}
+
+template <bool F32, int VEC>
+cudaError_t launch(VerifyParams& q, int B, cudaStream_t stream) {
+    return q.d != nullptr ? launch<F32, VEC, true>(q, B, stream) : launch<F32, VEC, false>(q, B, stream);
 }
 
 }  // namespace
@@ -319,15 +379,11 @@ cudaError_t launch_verify_drafts(const VerifyLaunch& a, cudaStream_t stream) {
     q.status = a.status;
     q.N = a.N;
     q.V = a.V;
-    const int cluster = kMaxCluster;
     const int per16 = a.f32 ? 4 : 8;
     const bool vec = a.V % per16 == 0 && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.d) % 16 == 0;
-    const int align = 32 * kWarps;                    // whole 32-element rows for each sixteenth of a chunk
-    const int64_t chunk = ((int64_t)a.V + cluster * kWarps - 1) / (cluster * kWarps);
-    q.chunk = (int32_t)((chunk + align - 1) / align * align);
-    if (a.f32) return vec ? launch<true, 4>(q, a.B, cluster, stream) : launch<true, 1>(q, a.B, cluster, stream);
-    return vec ? launch<false, 8>(q, a.B, cluster, stream) : launch<false, 1>(q, a.B, cluster, stream);
+    if (a.f32) return vec ? launch<true, 4>(q, a.B, stream) : launch<true, 1>(q, a.B, stream);
+    return vec ? launch<false, 8>(q, a.B, stream) : launch<false, 1>(q, a.B, stream);
 }
 
 }  // namespace nvfp4kv
