@@ -8,12 +8,20 @@
 //
 // Every step is one fp32 rounding; the keys are quantized from their fp32
 // values.  A head's row is held by D / 16 lanes, each with 8 elements of the
-// row's first half and the 8 elements D / 2 further on: the rotation's pairs
-// (i, i + D/2) and (2i, 2i + 1) then sit in one lane, and a 16-element block in
-// two neighbours (one shuffle for its amax).  A warp keeps one token's cos and
-// sin in registers and walks the token's heads.  Bound by HBM for prompt
-// chunks and by launch latency for a decode step: each element is read once
-// and written once.
+// rotated part's first half and the 8 elements R / 2 further on (or, behind the
+// rotated part, with 16 neighbours): the rotation's pairs (i, i + R/2) and
+// (2i, 2i + 1) then sit in one lane, and a 16-element block in one or two
+// neighbours (one shuffle for its amax).  A warp keeps one token's cos and sin
+// in registers and walks the token's heads, the next row's loads in flight.
+// Where R / 16 is odd a block would straddle the halves, and the pairs are
+// exchanged by shuffles instead (R = 64 that way: 53 us for 31 below).
+//
+// Measured (B200, bf16, head_dim 128): 2,048 tokens of 96 + 2 x 8 heads 28.4 us,
+// 3.9 TB/s of the 112 MB it has to move (17 us at 6.55 TB/s); the instructions
+// take as long (two elements each in the norm and the rotation, one at a time:
+// 37 us).  8 tokens of 32 + 2 x 8 heads: 4.4 us, launch and memory latency.
+// Blocks an SM for bf16: 6 without spills 30.6 us and 20.6 for 4 x 512 tokens, 7
+// with up to 32 bytes of them 28.4 and 16.7, 8 31.0 and 18.2.
 #include <cuda_bf16.h>
 
 #include "nvfp4kv_device.cuh"
@@ -23,7 +31,7 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kBlocks = 7;            // of 7 blocks an SM (bf16)
 
 enum RotKind { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2, kRotHalfPartial = 3 };
 
@@ -74,22 +82,39 @@ __device__ __forceinline__ uint32_t quantize_half(const float (&v)[8], float ama
     return word;
 }
 
+// eight elements as they lie in memory
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+struct Raw { uint4 w[F32 ? 2 : 1]; };
+template <bool F32>
+__device__ __forceinline__ Raw<F32> fetch8(const void* base, int64_t i) {
+    Raw<F32> r;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (F32 ? 4 : 2));
+    r.w[0] = __ldg(p);
+    if (F32) r.w[F32 ? 1 : 0] = __ldg(p + 1);
+    return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw<F32>& r, float (&v)[8]) {
     if (F32) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i);
-        const float4 a = __ldg(p), c = __ldg(p + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 u = r.w[F32 ? j : 0];
+            v[4 * j] = __uint_as_float(u.x); v[4 * j + 1] = __uint_as_float(u.y);
+            v[4 * j + 2] = __uint_as_float(u.z); v[4 * j + 3] = __uint_as_float(u.w);
+        }
     } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[2 * j] = __uint_as_float(w[j] << 16);
             v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
         }
     }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+    unpack8<F32>(fetch8<F32>(base, i), v);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -111,6 +136,30 @@ __device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8
     }
 }
 
+// Two fp32 operations at once, each rounded as alone.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// (a, b) -> (a c - b s, b c + a s) for two pairs, one rounding a step
+__device__ __forceinline__ void rotate2(float& a0, float& a1, float& b0, float& b1, float2 c, float2 s) {
+    const float2 a = make_float2(a0, a1), b = make_float2(b0, b1);
+    const float2 x = fma2(mul2(b, s), make_float2(-1.0f, -1.0f), mul2(a, c));
+    const float2 y = fma2(mul2(a, s), make_float2(1.0f, 1.0f), mul2(b, c));
+    a0 = x.x; a1 = x.y; b0 = y.x; b1 = y.y;
+}
+
 // (a, b) -> (a c - b s, b c + a s), one rounding a step
 __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
     const float x = a, y = b;
@@ -119,11 +168,16 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 }
 
 template <bool F32, int D, int ROT>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, ROT == kRotHalfPartial ? 4 : (F32 ? 5 : kBlocks)) qk_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LPR = D / 16;                       // lanes per row
     constexpr int RPW = 32 / LPR;                     // rows per warp pass
     const int lane = threadIdx.x & 31;
     const int t = lane % LPR, sub = lane / LPR;
+    // The lane's chunks of 8 elements: rotated ones with their partners, R / 2 further
+    // on; behind them whole blocks of 16.
+    const int hc = ROT == kRotHalf ? p.R / 16 : LPR;
+    const bool whole = t >= hc;
+    const int ca = whole ? 2 * t : t, cc = whole ? 2 * t + 1 : t + hc;
     const float st_k = *p.st_k, st_v = *p.st_v;
     const bool ok_k = st_k > 0.0f && st_k <= 3.4028234663852886e38f;
     const bool ok_v = st_v > 0.0f && st_v <= 3.4028234663852886e38f;
@@ -160,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
             const int half = p.R / 2;
             if (ROT == kRotHalf) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
+                for (int e = 0; !whole && e < 8; e += 4) {
                     *reinterpret_cast<float4*>(cs + e) = __ldg(reinterpret_cast<const float4*>(row + 8 * t + e));
                     *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(row + half + 8 * t + e));
                 }
@@ -213,27 +267,42 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
         }
 
         const int h_end = min(Ht, (part + 1) * p.heads_per_task);
+        // a row's two pieces are fetched while the row before is worked on
+        Raw<F32> ra = {}, rc = {};
+        auto fetch = [&](int h) {
+            if (h >= h_end) return;
+            const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+            const void* x = is_q ? p.xq : (is_k ? p.xk : p.xv);
+            const int64_t at = (int64_t)tok * (is_q ? p.sq : (is_k ? p.sk : p.sv)) +
+                               (int64_t)(is_q ? h : (is_k ? h - p.Hq : h - p.Hq - p.Hkv)) * D;
+            ra = fetch8<F32>(x, at + 8 * ca);
+            rc = fetch8<F32>(x, at + 8 * cc);
+        };
+        fetch(part * p.heads_per_task + sub);
+#pragma unroll 1
         for (int h0 = part * p.heads_per_task; h0 < h_end; h0 += RPW) {
             const int h = h0 + sub;
             const bool live = h < h_end;
             const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
             const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-            float a[8], c[8];                         // the lane's chunks t and t + LPR
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] = c[e] = 0.0f;
-            if (live) {
-                const void* x = is_q ? p.xq : (is_k ? p.xk : p.xv);
-                const int64_t at = (int64_t)tok * (is_q ? p.sq : (is_k ? p.sk : p.sv)) + (int64_t)(is_q ? h : hk) * D;
-                load8<F32>(x, at + 8 * t, a);
-                load8<F32>(x, at + D / 2 + 8 * t, c);
-            }
+            float a[8], c[8];                         // the lane's two chunks
+            unpack8<F32>(ra, a);
+            unpack8<F32>(rc, c);
+            fetch(h + RPW);
+            // elements taken two at a time: the neighbours, or of two interleaved pairs
+            // the first ones and the second ones
+            constexpr int S = ROT == kRotInterleaved ? 2 : 1;
+            auto first = [](int i) { return S == 2 ? 4 * (i >> 1) + (i & 1) : 2 * i; };
             const bool normed = is_q || is_k;         // values are left as they are
-            if (p.eps >= 0.0f) {
-                float ss = 0.0f;
+            if (p.eps >= 0.0f && h0 < p.Hq + p.Hkv) {
+                float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = __fmaf_rn(a[e], a[e], ss);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = __fmaf_rn(c[e], c[e], ss);
+                for (int i = 0; i < 4; ++i) {
+                    const int e = first(i);
+                    s2 = fma2(make_float2(a[e], a[e + S]), make_float2(a[e], a[e + S]), s2);
+                    s2 = fma2(make_float2(c[e], c[e + S]), make_float2(c[e], c[e + S]), s2);
+                }
+                float ss = s2.x + s2.y;
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
                 if (live && normed) {
@@ -241,41 +310,46 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
                     const void* w = is_q ? p.wq : p.wk;
                     float wa[8], wc[8];
                     if (w != nullptr) {
-                        load8<F32>(w, 8 * t, wa);
-                        load8<F32>(w, D / 2 + 8 * t, wc);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            a[e] = __fmul_rn(__fmul_rn(a[e], r), wa[e]);
-                            c[e] = __fmul_rn(__fmul_rn(c[e], r), wc[e]);
-                        }
+                        load8<F32>(w, 8 * ca, wa);
+                        load8<F32>(w, 8 * cc, wc);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            a[e] = __fmul_rn(a[e], r);
-                            c[e] = __fmul_rn(c[e], r);
-                        }
+                        for (int e = 0; e < 8; ++e) wa[e] = wc[e] = 1.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = first(i);
+                        const float2 r2 = make_float2(r, r);
+                        const float2 y = mul2(mul2(make_float2(a[e], a[e + S]), r2), make_float2(wa[e], wa[e + S]));
+                        const float2 z = mul2(mul2(make_float2(c[e], c[e + S]), r2), make_float2(wc[e], wc[e + S]));
+                        a[e] = y.x; a[e + S] = y.y;
+                        c[e] = z.x; c[e + S] = z.y;
                     }
                 }
             }
             if (ROT == kRotHalf) {
-                if (normed) {
+                if (normed && !whole) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) rotate(a[e], c[e], cs[e], sn[e]);
+                    for (int e = 0; e < 8; e += 2)
+                        rotate2(a[e], a[e + 1], c[e], c[e + 1], make_float2(cs[e], cs[e + 1]), make_float2(sn[e], sn[e + 1]));
                 }
             } else if (ROT == kRotInterleaved) {
                 if (normed) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (8 * t < p.R) rotate(a[2 * e], a[2 * e + 1], cs[e], sn[e]);
-                        if (8 * (t + LPR) < p.R) rotate(c[2 * e], c[2 * e + 1], cs[4 + e], sn[4 + e]);
+                    for (int e = 0; e < 4; e += 2) {
+                        if (8 * t < p.R)
+                            rotate2(a[2 * e], a[2 * e + 2], a[2 * e + 1], a[2 * e + 3], make_float2(cs[e], cs[e + 1]),
+                                    make_float2(sn[e], sn[e + 1]));
+                        if (8 * (t + LPR) < p.R)
+                            rotate2(c[2 * e], c[2 * e + 2], c[2 * e + 1], c[2 * e + 3], make_float2(cs[4 + e], cs[5 + e]),
+                                    make_float2(sn[4 + e], sn[5 + e]));
                     }
                 }
             } else if (ROT == kRotHalfPartial) {
                 // the partner chunk sits in another lane, in its first or second slot
-                const int hc = p.R / 16;
+                const int rc = p.R / 16;
                 float pa[8], pc[8];
-                const int ca = t, cc = t + LPR;
-                const int qa = ca < hc ? ca + hc : ca - hc, qc = cc < hc ? cc + hc : cc - hc;
+                const int qa = ca < rc ? ca + rc : ca - rc, qc = cc < rc ? cc + rc : cc - rc;
                 const int base = lane - t;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -289,12 +363,12 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
                 if (normed) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if (ca < 2 * hc) {
-                            if (ca < hc) rotate(a[e], pa[e], cs[e], sn[e]);
+                        if (ca < 2 * rc) {
+                            if (ca < rc) rotate(a[e], pa[e], cs[e], sn[e]);
                             else { rotate(pa[e], a[e], cs[e], sn[e]); }
                         }
-                        if (cc < 2 * hc) {
-                            if (cc < hc) rotate(c[e], pc[e], cs[8 + e], sn[8 + e]);
+                        if (cc < 2 * rc) {
+                            if (cc < rc) rotate(c[e], pc[e], cs[8 + e], sn[8 + e]);
                             else { rotate(pc[e], c[e], cs[8 + e], sn[8 + e]); }
                         }
                     }
@@ -302,8 +376,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
             }
             if (live && is_q) {
                 const int64_t at = ((int64_t)tok * p.Hq + h) * D;
-                store8<F32>(p.q_out, at + 8 * t, a);
-                store8<F32>(p.q_out, at + D / 2 + 8 * t, c);
+                store8<F32>(p.q_out, at + 8 * ca, a);
+                store8<F32>(p.q_out, at + 8 * cc, c);
             }
             if (h0 + RPW > p.Hq) {                    // some row of this pass is a key or a value
                 float ma = 0.0f, mc = 0.0f;
@@ -315,10 +389,18 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
                     na |= a[e] != a[e];
                     nc |= c[e] != c[e];
                 }
-                ma = fmaxf(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 1));
-                mc = fmaxf(mc, __shfl_xor_sync(0xFFFFFFFFu, mc, 1));
-                na |= __shfl_xor_sync(0xFFFFFFFFu, (int)na, 1) != 0;
-                nc |= __shfl_xor_sync(0xFFFFFFFFu, (int)nc, 1) != 0;
+                // the other chunk of the block: the neighbouring lane's, or this lane's
+                const float oa = __shfl_xor_sync(0xFFFFFFFFu, ma, 1), oc = __shfl_xor_sync(0xFFFFFFFFu, mc, 1);
+                const int flags = (na ? 1 : 0) | (nc ? 2 : 0), other = __shfl_xor_sync(0xFFFFFFFFu, flags, 1);
+                if (whole) {
+                    ma = mc = fmaxf(ma, mc);
+                    na = nc = flags != 0;
+                } else {
+                    ma = fmaxf(ma, oa);
+                    mc = fmaxf(mc, oc);
+                    na |= (other & 1) != 0;
+                    nc |= (other & 2) != 0;
+                }
                 if (live && !is_q && slot_ok) {
                     const float st = is_k ? st_k : st_v;
                     uint32_t sa, sc;
@@ -327,12 +409,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const __g
                     const int64_t slot = slot0 + (int64_t)hk * slot_step;
                     uint8_t* codes = (is_k ? p.kc : p.vc) + slot * (D / 2);
                     uint8_t* scales = (is_k ? p.ks : p.vs) + slot * (D / 16);
-                    *reinterpret_cast<uint32_t*>(codes + 4 * t) = wa;
-                    *reinterpret_cast<uint32_t*>(codes + D / 4 + 4 * t) = wc;
-                    if ((t & 1) == 0) {
-                        scales[t / 2] = (uint8_t)sa;
-                        scales[D / 32 + t / 2] = (uint8_t)sc;
-                    }
+                    *reinterpret_cast<uint32_t*>(codes + 4 * ca) = wa;
+                    *reinterpret_cast<uint32_t*>(codes + 4 * cc) = wc;
+                    if ((ca & 1) == 0) scales[ca / 2] = (uint8_t)sa;
+                    if ((cc & 1) == 0) scales[cc / 2] = (uint8_t)sc;
                 }
             }
         }
@@ -343,7 +423,7 @@ template <bool F32, int D>
 cudaError_t launch(const NormRopeParams& p, int rot, cudaStream_t stream) {
     const int64_t warps = p.tasks;
     int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t cap = 16L * device_sm_count();
+    const int64_t cap = kBlocks * (int64_t)device_sm_count();
     if (grid > cap) grid = cap;
     switch (rot) {
         case kRotNone: qk_norm_rope_append_kernel<F32, D, kRotNone><<<(unsigned)grid, kThreads, 0, stream>>>(p); break;
@@ -378,16 +458,23 @@ cudaError_t launch_qk_norm_rope_append(const NormRopeLaunch& a, cudaStream_t str
     const int rpw = 32 / (a.D / 16);
     const int Ht = a.Hq + 2 * a.Hkv;
     const int passes = (Ht + rpw - 1) / rpw;
-    // heads of one task: as many as leave every SM about 32 warps of tasks
-    const int64_t tokens = (int64_t)a.B * a.n;
-    int64_t per = tokens * passes / (32L * device_sm_count());
-    per = per < 1 ? 1 : (per > passes ? passes : per);
+    // Passes of one task: the split of the tokens' passes that the resident warps
+    // finish first, a task costing about two passes of its own (position, slot).
+    const int64_t tokens = (int64_t)a.B * a.n, warps = (int64_t)kBlocks * (kThreads / 32) * device_sm_count();
+    int64_t per = 1, best = INT64_MAX;
+    for (int parts = 1; parts <= passes; ++parts) {
+        const int64_t len = (passes + parts - 1) / parts, rounds = (tokens * parts + warps - 1) / warps;
+        if (rounds * (len + 2) < best) {
+            best = rounds * (len + 2);
+            per = len;
+        }
+    }
     p.heads_per_task = (int)per * rpw;
     p.tasks_per_token = (Ht + p.heads_per_task - 1) / p.heads_per_task;
     p.tasks = (uint32_t)(tokens * p.tasks_per_token);
     p.fd_tasks = FastDiv((uint32_t)p.tasks_per_token);
     p.fd_n = FastDiv((uint32_t)a.n);
-    const int rot = a.R == 0 ? kRotNone : (a.interleaved ? kRotInterleaved : (a.R == a.D ? kRotHalf : kRotHalfPartial));
+    const int rot = a.R == 0 ? kRotNone : (a.interleaved ? kRotInterleaved : (a.R % 32 == 0 ? kRotHalf : kRotHalfPartial));
     if (a.f32) return a.D == 128 ? launch<true, 128>(p, rot, stream) : launch<true, 64>(p, rot, stream);
     return a.D == 128 ? launch<false, 128>(p, rot, stream) : launch<false, 64>(p, rot, stream);
 }
