@@ -11,6 +11,7 @@ Formats and flow follow "NVIDIA解説: NVFP4 KV Cacheで長コンテキストLLM
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 from typing import Optional
@@ -364,16 +365,23 @@ def _need_kind(k, v, kind):
         raise TypeError("k and v must be %s" % kind.__name__)
 
 
-def _like_rows(x: torch.Tensor, counts, dtype) -> torch.Tensor:
+def _allocating(stream):
+    """Tensors that a call makes for itself are made on its stream: filled there before
+    its kernels, and not given to another stream's work while they run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _like_rows(x: torch.Tensor, counts, dtype, stream) -> torch.Tensor:
     """A dense output like x; with `counts` the rows behind them are not written: zeros."""
-    return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=dtype, device=x.device)
+    with _allocating(stream):
+        return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=dtype, device=x.device)
 
 
 def _qk_norm_rope_append(func, kind, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps, rope_table,
                          interleaved, positions, n_valid, q_out, new_lens, status, stream):
     _need_kind(k, v, kind)
     if q_out is None:
-        q_out = _like_rows(x_q, n_valid, x_q.dtype)
+        q_out = _like_rows(x_q, n_valid, x_q.dtype, stream)
     st = _native.binding().qk_norm_rope_append(
         *_target(stream), kind is PagedKVPlane, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps,
         rope_table, interleaved, positions, n_valid, q_out, new_lens, status)
@@ -421,13 +429,14 @@ def _tree_attention(func, kind, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree
                     out_dtype, workspace, status, stream):
     _need_kind(k, v, kind)
     if out is None:
-        out = _like_rows(q, n_nodes, out_dtype)
+        out = _like_rows(q, n_nodes, out_dtype, stream)
     if workspace is None:
         B, N, H_q, D = q.shape
         size = nvfp4_tree_attention_workspace(B, N, H_q, k.codes.shape[1], D)
         if size == 0:
             raise ValueError("unsupported attention shape")
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        with _allocating(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     st = _native.binding().tree_attention(
         *_target(stream), kind is PagedKVPlane, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree_mask, n_nodes,
         softmax_scale, out, workspace, status)
@@ -474,9 +483,10 @@ def nvfp4_verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.
     if path is None or n_accepted is None or next_token is None:
         B, N, _ = target_probs.shape
         dev = target_probs.device
-        path = torch.full((B, N), -1, dtype=torch.int32, device=dev) if path is None else path
-        n_accepted = torch.zeros(B, dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
-        next_token = torch.full((B,), -1, dtype=torch.int32, device=dev) if next_token is None else next_token
+        with _allocating(stream):
+            path = torch.full((B, N), -1, dtype=torch.int32, device=dev) if path is None else path
+            n_accepted = torch.zeros(B, dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
+            next_token = torch.full((B,), -1, dtype=torch.int32, device=dev) if next_token is None else next_token
     st = _native.binding().verify_drafts(*_target(stream), target_probs, draft_probs, tokens, parents, u_accept, u_sample,
                                          n_nodes, path, n_accepted, next_token, status)
     if st:

@@ -641,3 +641,40 @@ def test_step_captured_replayed_and_on_another_stream(nv):
     torch.cuda.synchronize()
     for x, y in zip(b.state(), c.state()):
         assert torch.equal(x, y)
+
+
+def test_outputs_made_by_a_call_belong_to_its_stream(nv):
+    """With `stream` given and no outputs or workspace, what the call makes for
+    itself is neither filled late by the current stream nor reused by it early."""
+    torch.manual_seed(5)
+    c, s = synthetic.random_planes(11, 2, 2, 640, 128, max_scale_byte=0x50)
+    k, v = nv.KVPlane(c.cuda(), s.cuda()), nv.KVPlane(c.cuda(), s.cuda())
+    q, sc = torch.randn(2, 8, 4, 128, device="cuda").bfloat16(), torch.tensor([0.01], device="cuda")
+    x = torch.randn(2, 8, 2, 128, device="cuda").bfloat16()
+    start, counts = i32([600, 300]), i32([8, 5])
+    p = torch.softmax(torch.randn(2, 8, 3000, device="cuda"), -1)
+    d = torch.softmax(torch.randn(2, 8, 3000, device="cuda"), -1)
+    tok, par = torch.randint(0, 3000, (2, 8), device="cuda", dtype=torch.int32), i32([-1, 0, 0, 1, 1, 2, 2, 3])
+    ua, us = torch.rand(2, 8, device="cuda"), torch.rand(2, device="cuda")
+
+    def calls(stream):
+        o = nv.nvfp4_tree_attention(q, k, v, sc, sc, start, n_nodes=counts, stream=stream)
+        y = nv.nvfp4_qk_norm_rope_append(q, x, x, start, sc, sc, k, v, n_valid=counts, stream=stream)
+        return [o, y, *nv.nvfp4_verify_drafts(p, d, tok, par, ua, us, n_nodes=counts, stream=stream)]
+    calls(None)                                       # the nodes' own slots hold what each call below appends
+    want = calls(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                     # the current stream is late ..
+    late = calls(side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                 # .. or early
+    early = calls(side)
+    size = nv.nvfp4_tree_attention_workspace(2, 8, 4, 2, 128)
+    junk = [torch.full((size // 4,), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    del junk
+    for got in (late, early):
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
