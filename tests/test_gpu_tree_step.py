@@ -678,3 +678,18 @@ def test_outputs_made_by_a_call_belong_to_its_stream(nv):
     for got in (late, early):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("N,g", [(8, 4), (33, 1), (16, 4), (13, 5), (32, 4), (43, 3), (64, 4), (257, 1)])
+def test_tree_attention_row_counts(nv, N, g, D, bf16):
+    """Rows 32, 33, 64, 65, 128, 129, 256, 257 of a KV head: where their copies and blocks change."""
+    run_tree(nv, 2, N, 2 * g, 2, D, [700, 130], "tree", bf16, seed=N + g)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_tree_attention_long_segments(nv, D):
+    """Ranges of more than 32 tiles of one unit (on 148 SMs): the fp32 outputs' sums are
+    flushed and joined, next to units that the ranges cut."""
+    run_tree(nv, 18, 2, 16, 8, D, [4400 + 7 * b for b in range(18)], "chain", False, seed=3, oracle_seqs=[0, 9, 17])
