@@ -1,6 +1,9 @@
 """Host-side checks of the tree-step entry points: every call below is refused,
 or is a no-op, before it reaches the GPU."""
 import ctypes
+import os
+import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -165,3 +168,24 @@ def test_reference_forms_agree_with_closed_forms():
     assert ref.verify(p, d, [0, 1], [-1, 0], [0, 0.4], 0.49, 2) == ([0], 0)
     y, _ = ref.norm_rope(np.array([3.0, 0, 4.0, 0] + [0.0] * 12), None, 0.0, np.array([0.0] * 8 + [1.0] * 8), True)
     assert np.allclose(y[:4], [0, 3 / np.sqrt(25 / 16), 0, 4 / np.sqrt(25 / 16)])
+
+
+def test_tree_attention_kernels_fit_their_register_split(tmp_path):
+    """No stack frame or spill, and as many registers at launch as the warpgroups' shares
+    add up to: a larger sum would wait for registers that nobody gives back."""
+    src = os.path.join(native_build.CSRC, "nvfp4kv_tree_attention_tc.cu")
+    cmd = [native_build.nvcc(), *[f for f in native_build.NVCC_FLAGS if f != "-shared"], "-c", "-Xptxas", "-v",
+           "-I", native_build.INCLUDE, "-o", str(tmp_path / "tree.o"), src]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+    except FileNotFoundError:
+        pytest.skip("nvcc not available")
+    assert r.returncode == 0, r.stderr[-2000:]
+    found = re.findall(r"Compiling entry function '[^']*tree_attention_tc_kernelINS0_3CfgILi(\d+)ELi(\d)E[^']*'.*?\n"
+                       r".*?(\d+) bytes stack frame, (\d+) bytes spill stores, (\d+) bytes spill loads.*?"
+                       r"Used (\d+) registers", r.stderr, flags=re.S)
+    assert len(found) == 8
+    for _, rb, stack, stores, loads, regs in found:
+        assert (stack, stores, loads) == ("0", "0", "0")
+        threads, shares = (896, 256 * 112 + 128 * 56 + 512 * 56) if rb == "1" else (640, 256 * 136 + 128 * 64 + 256 * 72)
+        assert shares <= threads * int(regs) <= 65536
