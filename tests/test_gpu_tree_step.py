@@ -693,3 +693,30 @@ def test_tree_attention_long_segments(nv, D):
     """Ranges of more than 32 tiles of one unit (on 148 SMs): the fp32 outputs' sums are
     flushed and joined, next to units that the ranges cut."""
     run_tree(nv, 18, 2, 16, 8, D, [4400 + 7 * b for b in range(18)], "chain", False, seed=3, oracle_seqs=[0, 9, 17])
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,S", [(2, 8, 8, 2, 128, 5000), (1, 64, 8, 2, 128, 9000), (3, 40, 12, 4, 64, 3000)])
+def test_tree_attention_times_out_anywhere_and_recovers(nv, B, N, Hq, Hkv, D, S):
+    """Limits between giving up at once and never: whichever waits run out, the call
+    returns, says so, and the next one is right."""
+    S16 = (S + N + 15) // 16 * 16
+    c, s = synthetic.random_planes(4, B, Hkv, S16, D, max_scale_byte=0x50)
+    k, v = nv.KVPlane(c.cuda(), s.cuda()), nv.KVPlane(c.cuda(), s.cuda())
+    q, sc = torch.randn(B, N, Hq, D, device="cuda").bfloat16(), torch.tensor([0.01], device="cuda")
+    start = i32([S] * B)
+    for dtype in (torch.float32, torch.bfloat16):
+        want = nv.nvfp4_tree_attention(q, k, v, sc, sc, start, out_dtype=dtype)
+        for limit in (0, 1, 0, 2, 3):
+            st = status()
+            try:
+                nv.nvfp4_set_wait_limit(limit)
+                got = nv.nvfp4_tree_attention(q, k, v, sc, sc, start, out_dtype=dtype, status=st)
+                torch.cuda.synchronize()
+            finally:
+                nv.nvfp4_set_wait_limit(-1)
+            assert st.item() in (0, nv.NVFP4_ERR_TIMEOUT)
+            if st.item() == 0:
+                assert torch.equal(got, want)
+            st = status()
+            assert torch.equal(nv.nvfp4_tree_attention(q, k, v, sc, sc, start, out_dtype=dtype, status=st), want)
+            assert st.item() == 0
