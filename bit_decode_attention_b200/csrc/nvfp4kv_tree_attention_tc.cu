@@ -46,16 +46,18 @@
 // Measured (B200, head_dim 128; a tile's raw bytes take 774 clocks of an SM's share
 // of 6.55 TB/s, its MMAs 512 with one row block and 1,024 with two):
 //   128 sequences x 8 KV heads, up to 8 nodes x 4 heads, 1,024 to 8,192 tokens:
-//     374 us, 2,140 clocks a tile.  A loop of waits paces it, for each of two buffers:
+//     358 us, 2,140 clocks a tile.  A loop of waits paces it, for each of two buffers:
 //     dequant 2,300 to 2,900 (the SM issues 0.59 instructions a clock and scheduler,
-//     the integer pipe is 58% busy), then 1,000 of MMA issue and completion
-//   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 102 us, 4,700 clocks
+//     the integer pipe is 58% busy), then 1,000 of MMA issue and completion.  A
+//     unit's end and the next one's queries take 9,000 clocks beside its tiles.
+//   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 101 us, 4,700 clocks
 //     a tile; the softmax paces it: 3,300 of arithmetic (256 x 128 exponentials are
 //     2,048 at the SM's 16 a clock) and 1,400 between P and the next scores
-// Tried and slower on the first: rows on N (one exchange of maxima per tile: 394 us),
-// 8 dequant warps in place of 16 (451 us against 433 then), all 16 on each tile
-// (438 us), e4m3 keys with queries in two e4m3/e5m2 terms and a third value buffer
-// (377 us: 10% fewer integer instructions, more code than the instruction cache holds).
+// Tried and slower on the first, each against its day's figure: rows on N, with one
+// exchange of maxima per tile (394 us); 8 dequant warps in place of 16 (451 us, 433);
+// all 16 on each tile (438, 370); e4m3 keys with queries in two e4m3/e5m2 terms and a
+// third value buffer (377, 370: 10% fewer integer instructions, but more code than
+// the instruction cache holds).  On the second: the next scores read ahead (107, 102).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -197,7 +199,7 @@ __device__ __forceinline__ void regs_dec() {
 // where the tensor cores read it) comes before what the others do after.  Producers
 // and the MMA warp both wait: if a producer's warp only arrived, one that came again
 // early (as the roles do once a wait has given up) would stand for another warp.
-// (Arriving only was no faster: 371 us for 368 on the ragged batch above.)
+// (Arriving only was no faster: 371 us for 368 then on the ragged batch above.)
 __device__ __forceinline__ void bar_sync(int id, int n) {
     asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -753,14 +755,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
             const bool whole = s.tiles == s.unit_tiles;
             float* const slot = p.partials + (int64_t)(2 * blockIdx.x + (s.tile0 > 0 ? 0 : 1)) * C::kSlot;
             // m and l of the row over its copies and, unless each group has its own rows, groups
-            float m_all = -INFINITY, l_all = 0.0f;
-            for (int g = dual ? h : 0; g < (dual ? h + 1 : 2); ++g)
-                for (int q = 0; q < 1 << lg_parts; ++q) m_all = fmaxf(m_all, sm.ml[g][0][lr + q * rows_per]);
-            for (int g = dual ? h : 0; g < (dual ? h + 1 : 2); ++g)
-                for (int q = 0; q < 1 << lg_parts; ++q) {
-                    const float mq = sm.ml[g][0][lr + q * rows_per];
-                    l_all += mq == -INFINITY ? 0.0f : sm.ml[g][1][lr + q * rows_per] * fast_exp2(mq - m_all);
-                }
+            float m8[8], m_all = -INFINITY, l_all = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int g = i >> 2, q = i & 3;
+                m8[i] = (!dual || g == h) && q < 1 << lg_parts ? sm.ml[g][0][lr + q * rows_per] : -INFINITY;
+                m_all = fmaxf(m_all, m8[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (m8[i] != -INFINITY)
+                    l_all = __fmaf_rn(sm.ml[i >> 2][1][lr + (i & 3) * rows_per], fast_exp2(m8[i] - m_all), l_all);
             const float inv = whole ? (l_all > 0.0f ? 1.0f / l_all : 0.0f) : 1.0f;
             // factors of the groups' O (of this copy); 0 where a group saw nothing: O is anything then
             float fo[2], ff[2];                       // of O, and of what was flushed of it
@@ -787,11 +792,27 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
             }
             const int64_t at =
                 (((int64_t)s.b * p.N + nd) * p.Hq + (int64_t)s.hk * p.g + (gr0 + row - nd * p.g)) * D;
+            // four columns of the row: fp32 to the partial (or the output), or bf16
+            float* const dst = whole && TWO ? reinterpret_cast<float*>(p.out) + at : slot + 4 * row;
+            const int dst_step = whole && TWO ? 4 : 4 * RB * T;
+            auto store4 = [&](int col, float4 z) {
+                if (!live) return;
+                if (!TWO && whole) {
+                    const __nv_bfloat162 e = __floats2bfloat162_rn(z.x, z.y), f = __floats2bfloat162_rn(z.z, z.w);
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at + col) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&e), *reinterpret_cast<const uint32_t*>(&f));
+                } else {
+                    *reinterpret_cast<float4*>(dst + (col / 4) * dst_step) = z;
+                }
+            };
             // Columns 16 at a time: group h takes every other 16 (all of them when the rows
-            // are its own).  The copies' sums meet in the query buffer, [copy][column][row].
-            // (Two buffers where the query buffer holds them: one barrier less.)
+            // are its own).  The copies' sums meet in the query buffer, 64 bytes a row, its
+            // 16-byte pieces permuted so that eight rows' fill all banks; each copy sums
+            // its share of the pieces over the copies.  (Two buffers where the query buffer
+            // holds them: one barrier less.)
             constexpr bool TWOBUF = sizeof(sm.q[0]) >= 4 * T * 16 * sizeof(float);
-            float* const meet0 = reinterpret_cast<float*>(sm.q[0]) + h * (T * 16);
+            float4* const meet0 = reinterpret_cast<float4*>(sm.q[0]) + h * (T * 4);
+            const int turn = (r >> 1) & 3;
 #pragma unroll 1
             for (int c = dual ? 0 : 16 * h; c < D; c += dual ? 16 : 32) {
                 float y[16];
@@ -812,39 +833,32 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
                         }
                     }
                 }
-                if (lg_parts > 0) {
-                    float* const meet = meet0 + (TWOBUF && (c & 32) ? 2 * T * 16 : 0);
+                if (lg_parts == 0) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) meet[j * T + r] = y[j];
-                    bar_sync(kBarMeet + h, 128);
-                    if (part == 0 && live)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            y[j] += meet[j * T + lr + rows_per];
-                            if (lg_parts == 2) y[j] += meet[j * T + lr + 64] + meet[j * T + lr + 96];
-                        }
-                    if (!TWOBUF) bar_sync(kBarMeet + h, 128);   // read before it is written again
-                }
-                if (!live || part > 0) continue;
-                if (!whole) {
-                    float4* dst = reinterpret_cast<float4*>(slot) + (c / 4) * (RB * T) + row;
+                    for (int j = 0; j < 16; j += 4) store4(c + j, make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+                } else {
+                    float4* const meet = meet0 + (TWOBUF && (c & 32) ? 2 * T * 4 : 0);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        dst[j * (RB * T)] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                } else if (TWO) {
-                    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + c);
+                        meet[4 * r + (j ^ turn)] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    bar_sync(kBarMeet + h, 128);
+                    // piece 2 part + i / 2 of copy i % 2, or piece part of copy i
+                    float4 z[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at + c);
-                    uint32_t x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-                        x[j] = *reinterpret_cast<const uint32_t*>(&z);
+                    for (int i = 0; i < 4; ++i) {
+                        const int from = lr + (lg_parts == 1 ? (i & 1) * 64 : i * 32);
+                        const int piece = lg_parts == 1 ? 2 * part + (i >> 1) : part;
+                        z[i] = meet[4 * from + (piece ^ turn)];
                     }
-                    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-                    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+                    auto add4 = [](float4 u, float4 v) { return make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w); };
+                    const float4 lo = add4(z[0], z[1]), hi2 = add4(z[2], z[3]);
+                    if (lg_parts == 1) {
+                        store4(c + 8 * part, lo);
+                        store4(c + 8 * part + 4, hi2);
+                    } else {
+                        store4(c + 4 * part, add4(lo, hi2));
+                    }
+                    if (!TWOBUF) bar_sync(kBarMeet + h, 128);   // read before it is written again
                 }
             }
             if (!whole && live && part == 0 && (dual || h == 0)) {
