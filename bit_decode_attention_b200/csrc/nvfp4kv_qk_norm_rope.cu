@@ -21,7 +21,7 @@
 // take as long (two elements each in the norm and the rotation, one at a time:
 // 37 us).  8 tokens of 32 + 2 x 8 heads: 4.4 us, launch and memory latency.
 // Blocks an SM for bf16: 6 without spills 30.6 us and 20.6 for 4 x 512 tokens, 7
-// with up to 32 bytes of them 28.4 and 16.7, 8 31.0 and 18.2.
+// with up to 32 bytes of them 28.4 and 16.7, 8 31.0 and 18.2.  fp32: 41 us for 34.
 #include <cuda_bf16.h>
 
 #include "nvfp4kv_device.cuh"
@@ -31,9 +31,12 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kThreads = 128, kBlocks = 7;            // of 7 blocks an SM (bf16)
+constexpr int kThreads = 128;
 
 enum RotKind { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2, kRotHalfPartial = 3 };
+
+// resident blocks of an SM, which the registers are cut for
+__host__ __device__ constexpr int blocks_per_sm(bool f32, int rot) { return rot == kRotHalfPartial ? 4 : (f32 ? 5 : 7); }
 
 struct NormRopeParams {
     const void *xq, *xk, *xv;
@@ -168,7 +171,7 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 }
 
 template <bool F32, int D, int ROT>
-__global__ void __launch_bounds__(kThreads, ROT == kRotHalfPartial ? 4 : (F32 ? 5 : kBlocks)) qk_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(F32, ROT)) qk_norm_rope_append_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LPR = D / 16;                       // lanes per row
     constexpr int RPW = 32 / LPR;                     // rows per warp pass
     const int lane = threadIdx.x & 31;
@@ -423,7 +426,7 @@ template <bool F32, int D>
 cudaError_t launch(const NormRopeParams& p, int rot, cudaStream_t stream) {
     const int64_t warps = p.tasks;
     int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t cap = kBlocks * (int64_t)device_sm_count();
+    const int64_t cap = blocks_per_sm(F32, rot) * (int64_t)device_sm_count();
     if (grid > cap) grid = cap;
     switch (rot) {
         case kRotNone: qk_norm_rope_append_kernel<F32, D, kRotNone><<<(unsigned)grid, kThreads, 0, stream>>>(p); break;
@@ -458,9 +461,10 @@ cudaError_t launch_qk_norm_rope_append(const NormRopeLaunch& a, cudaStream_t str
     const int rpw = 32 / (a.D / 16);
     const int Ht = a.Hq + 2 * a.Hkv;
     const int passes = (Ht + rpw - 1) / rpw;
+    const int rot = a.R == 0 ? kRotNone : (a.interleaved ? kRotInterleaved : (a.R % 32 == 0 ? kRotHalf : kRotHalfPartial));
     // Passes of one task: the split of the tokens' passes that the resident warps
     // finish first, a task costing about two passes of its own (position, slot).
-    const int64_t tokens = (int64_t)a.B * a.n, warps = (int64_t)kBlocks * (kThreads / 32) * device_sm_count();
+    const int64_t tokens = (int64_t)a.B * a.n, warps = (int64_t)blocks_per_sm(a.f32, rot) * (kThreads / 32) * device_sm_count();
     int64_t per = 1, best = INT64_MAX;
     for (int parts = 1; parts <= passes; ++parts) {
         const int64_t len = (passes + parts - 1) / parts, rounds = (tokens * parts + warps - 1) / warps;
@@ -474,7 +478,6 @@ cudaError_t launch_qk_norm_rope_append(const NormRopeLaunch& a, cudaStream_t str
     p.tasks = (uint32_t)(tokens * p.tasks_per_token);
     p.fd_tasks = FastDiv((uint32_t)p.tasks_per_token);
     p.fd_n = FastDiv((uint32_t)a.n);
-    const int rot = a.R == 0 ? kRotNone : (a.interleaved ? kRotInterleaved : (a.R % 32 == 0 ? kRotHalf : kRotHalfPartial));
     if (a.f32) return a.D == 128 ? launch<true, 128>(p, rot, stream) : launch<true, 64>(p, rot, stream);
     return a.D == 128 ? launch<false, 128>(p, rot, stream) : launch<false, 64>(p, rot, stream);
 }
