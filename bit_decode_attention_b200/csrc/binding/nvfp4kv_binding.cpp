@@ -145,7 +145,7 @@ struct Cache {
 };
 
 // elements between tokens of x [B][n][H][D]: dense heads, evenly spaced tokens
-// (a slice of a packed projection has them)
+// (a slice of a packed projection has them; a tensor expanded over tokens or sequences has not)
 const void* rows(PyObject* o, int cur, at::ScalarType type, int64_t B, int64_t n, int64_t H, int64_t D, const char* name,
                  int64_t& step) {
     const at::Tensor& t = tensor_of(o, name);
@@ -158,7 +158,9 @@ const void* rows(PyObject* o, int cur, at::ScalarType type, int64_t B, int64_t n
     if (t.numel() == 0) return t.data_ptr();
     const auto s = t.strides();
     step = n > 1 ? s[1] : (B > 1 ? s[0] : H * D);
-    if ((D > 1 && s[3] != 1) || (H > 1 && s[2] != D) || (B > 1 && n > 1 && s[0] != n * s[1]))
+    // a step below a token's row is a broadcast (0, which the C call takes for dense) or an overlap
+    if ((D > 1 && s[3] != 1) || (H > 1 && s[2] != D) || (B > 1 && n > 1 && s[0] != n * s[1]) ||
+        (B * n > 1 && step < H * D))
         fail(PyExc_ValueError, std::string(name) + " must have dense heads and evenly spaced tokens");
     return t.data_ptr();
 }

@@ -149,6 +149,45 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib, monkeypatch):
         nv.KVPlaneList([])
 
 
+def binding_append(nv, xq, xk, xv, B, H, D=64, eps=float("nan"), interleaved=False):
+    """The binding's checks of an append, on host tensors (device -1); eps NaN is refused by
+    the library, before any launch: a call that passes the binding returns INVALID."""
+    pl = nv.KVPlane(torch.zeros(B, H, 16, D // 2, dtype=torch.uint8), torch.zeros(B, H, 16, D // 16, dtype=torch.uint8))
+    one, start = torch.ones(1), torch.zeros(B, dtype=torch.int32)
+    out = torch.empty(xq.shape, dtype=xq.dtype)
+    return _native.binding().qk_norm_rope_append(-1, 0, False, xq, xk, xv, start, one, one, pl, pl, None, None, eps, None,
+                                                 interleaved, None, None, out, None, None)
+
+
+@pytest.mark.parametrize("B,n,from_shape", [(2, 3, (1, 1)), (2, 1, (1, 1)), (1, 3, (1, 1)), (2, 3, (1, 3)), (2, 3, (2, 1))])
+def test_binding_refuses_broadcast_inputs(lib, B, n, from_shape):
+    """Memory that holds fewer rows than the shape says (a step of 0 between tokens)."""
+    import bit_decode_attention_b200 as nv
+    full = torch.zeros(B, n, 2, 64)
+    few = torch.zeros(*from_shape, 2, 64).expand(B, n, 2, 64)
+    assert binding_append(nv, full, full, full, B, 2) == INVALID
+    for at in range(3):
+        x = [full] * 3
+        x[at] = few
+        with pytest.raises(ValueError, match="evenly spaced"):
+            binding_append(nv, *x, B, 2)
+    # steps below a token's row, without being 0
+    over = torch.zeros(2 * 64 + 16 * (B * n - 1) + 64)
+    with pytest.raises(ValueError, match="evenly spaced"):
+        binding_append(nv, over.as_strided((B, n, 2, 64), (16 * n, 16, 64, 1)), full, full, B, 2)
+
+
+def test_binding_takes_rows_of_one_token_and_packed_rows(lib):
+    import bit_decode_attention_b200 as nv
+    one = torch.zeros(64).expand(1, 1, 1, 64)
+    assert binding_append(nv, one, one, one, 1, 1) == INVALID
+    packed = torch.zeros(2, 3, 4, 64)
+    q, k, v = packed[:, :, :2], packed[:, :, 2:3], packed[:, :, 3:]
+    assert binding_append(nv, q, k, v, 2, 1) == INVALID
+    empty = torch.zeros(2, 0, 1, 64)
+    assert binding_append(nv, empty, empty, empty, 2, 1) == INVALID
+
+
 def test_reference_forms_agree_with_closed_forms():
     # the references the GPU tests compare with, on cases worked by hand
     m = ref.ancestors(ref.parents_of("star", 4))
