@@ -171,6 +171,12 @@ long as_long(PyObject* o) {
     return v;
 }
 
+bool as_bool(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Failed{};
+    return v != 0;
+}
+
 float as_float(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Failed{};
@@ -212,7 +218,7 @@ int norm_rope(PyObject* const* a, int cur, F call) {
     }
     return call(q, k, v, dt, narrow(n), narrow(Hq), sq, sk, sv, need_or_null(a[11], cur, type, {D}, "w_q"),
                 need_or_null(a[12], cur, type, {D}, "w_k"), as_float(a[13]), table, narrow(P), narrow(R),
-                PyObject_IsTrue(a[15]), ints_or_null(a[16], cur, {B, n}, "positions"),
+                as_bool(a[15]), ints_or_null(a[16], cur, {B, n}, "positions"),
                 ints(a[6], cur, {B}, "start_pos"), ints_or_null(a[17], cur, {B}, "n_valid"),
                 ints_or_null(a[19], cur, {B}, "new_lens"),
                 static_cast<const float*>(scalar(a[7], cur, at::kFloat, "s_tensor_k")),
@@ -296,14 +302,14 @@ PyObject* entry(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, F f) {
 
 PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(a, n, 21, [&](int cur) {
-        return PyObject_IsTrue(a[2]) ? norm_rope<nvfp4_kv_paged_plane>(a, cur, nvfp4_qk_norm_rope_append_paged)
+        return as_bool(a[2]) ? norm_rope<nvfp4_kv_paged_plane>(a, cur, nvfp4_qk_norm_rope_append_paged)
                                      : norm_rope<nvfp4_kv_plane>(a, cur, nvfp4_qk_norm_rope_append);
     });
 }
 
 PyObject* py_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(a, n, 15, [&](int cur) {
-        return PyObject_IsTrue(a[2]) ? tree<nvfp4_kv_paged_plane>(a, cur, nvfp4_tree_attention_paged)
+        return as_bool(a[2]) ? tree<nvfp4_kv_paged_plane>(a, cur, nvfp4_tree_attention_paged)
                                      : tree<nvfp4_kv_plane>(a, cur, nvfp4_tree_attention);
     });
 }
@@ -314,7 +320,7 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyObject* py_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(a, n, 11, [&](int cur) {
-        return PyObject_IsTrue(a[2]) ? commit<nvfp4_kv_paged_plane>(a, cur, nvfp4_kv_commit_path_paged)
+        return as_bool(a[2]) ? commit<nvfp4_kv_paged_plane>(a, cur, nvfp4_kv_commit_path_paged)
                                      : commit<nvfp4_kv_plane>(a, cur, nvfp4_kv_commit_path);
     });
 }
@@ -324,7 +330,7 @@ PyObject* py_planes(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         if (n != 3) fail(PyExc_TypeError, "wrong number of arguments");
         const int cur = (int)as_long(a[0]);
-        const bool paged = PyObject_IsTrue(a[1]);
+        const bool paged = as_bool(a[1]);
         const Ref seq(PySequence_Fast(a[2], "planes must be a sequence"));
         const Py_ssize_t m = PySequence_Fast_GET_SIZE(seq.o);
         std::string bytes;

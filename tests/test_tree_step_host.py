@@ -188,6 +188,15 @@ def test_binding_takes_rows_of_one_token_and_packed_rows(lib):
     assert binding_append(nv, empty, empty, empty, 2, 1) == INVALID
 
 
+def test_binding_passes_on_a_failing_truth_value(lib):
+    """`interleaved` without a truth value: its own error, and no call."""
+    import bit_decode_attention_b200 as nv
+    x = torch.zeros(1, 2, 1, 64)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        binding_append(nv, x, x, x, 1, 1, interleaved=torch.zeros(2))
+    assert binding_append(nv, x, x, x, 1, 1, interleaved=torch.ones(1)) == INVALID
+
+
 def test_reference_forms_agree_with_closed_forms():
     # the references the GPU tests compare with, on cases worked by hand
     m = ref.ancestors(ref.parents_of("star", 4))
