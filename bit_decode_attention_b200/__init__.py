@@ -497,10 +497,11 @@ def nvfp4_verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.
 class KVPlaneList:
     """The planes of a cache (all layers' K and V: KVPlane, or PagedKVPlane that
     share one block table), checked and laid out once for nvfp4_kv_commit_path.
-    Holds the planes; a plane whose tensors are replaced needs a new list."""
+    Holds the planes, and the tensors they had when the list was made, which stay
+    the ones that are moved: a plane whose tensors are replaced needs a new list."""
 
     def __init__(self, planes):
-        self.planes = list(planes)
+        self.planes = tuple(planes)
         if not self.planes:
             raise ValueError("a plane list needs at least one plane")
         self.kind = type(self.planes[0])
@@ -514,9 +515,12 @@ class KVPlaneList:
         data, self.B = _native.binding().planes(self.device, self.kind is PagedKVPlane, self.planes)
         self._structs = ctypes.create_string_buffer(data, len(data))
         self.address = ctypes.addressof(self._structs)
+        self._count = len(self.planes)
+        # what the structs point at, whatever becomes of the planes' attributes
+        self._tensors = [tuple(vars(p).values()) for p in self.planes]
 
     def __len__(self):
-        return len(self.planes)
+        return self._count
 
 
 def _commit_path(func, kind, planes, start_pos, path, n_accepted, new_lens, status, stream):
@@ -527,7 +531,7 @@ def _commit_path(func, kind, planes, start_pos, path, n_accepted, new_lens, stat
     cur, handle = _target(stream)
     if planes.device != cur:
         raise ValueError("planes must be on the current CUDA device (%d), got %d" % (cur, planes.device))
-    st = _native.binding().commit_path(cur, handle, kind is PagedKVPlane, planes.address, len(planes.planes), planes.B,
+    st = _native.binding().commit_path(cur, handle, kind is PagedKVPlane, planes.address, len(planes), planes.B,
                                        start_pos, path, n_accepted, new_lens, status)
     if st:
         _native.check(func, st)

@@ -197,6 +197,50 @@ def test_binding_passes_on_a_failing_truth_value(lib):
     assert binding_append(nv, x, x, x, 1, 1, interleaved=torch.ones(1)) == INVALID
 
 
+def test_plane_list_keeps_what_its_addresses_name(lib, monkeypatch):
+    """The structs are laid out once: planes that a caller adds to the list later, or tensors
+    replaced in one, must not change what the call reads or free what it points at."""
+    import gc
+    import weakref
+    import bit_decode_attention_b200 as nv
+
+    class OnDevice(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    real, seen = _native.binding(), []
+
+    class Binding:
+        @staticmethod
+        def planes(device, paged, planes):
+            return real.planes(-1, paged, planes)
+
+        @staticmethod
+        def commit_path(device, stream, paged, address, count, *rest):
+            seen.append((address, count))
+            return 0
+
+    monkeypatch.setattr(_native, "binding", lambda: Binding)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    new = lambda: nv.KVPlane(torch.zeros(1, 1, 16, 64, dtype=torch.uint8).as_subclass(OnDevice),
+                             torch.zeros(1, 1, 16, 8, dtype=torch.uint8).as_subclass(OnDevice))
+    mine = [new(), new()]
+    planes = nv.KVPlaneList(mine)
+    codes = weakref.ref(mine[0].codes)
+    mine.append(new())
+    try:
+        planes.planes.append(new())
+    except AttributeError:
+        pass                                               # not a list any more
+    assert len(planes) == 2
+    nv.nvfp4_kv_commit_path(planes, None, None, None)
+    assert seen == [(planes.address, 2)]
+    mine[0].codes = new().codes
+    gc.collect()
+    assert codes() is not None                             # the structs still name this memory
+
+
 def test_reference_forms_agree_with_closed_forms():
     # the references the GPU tests compare with, on cases worked by hand
     m = ref.ancestors(ref.parents_of("star", 4))
