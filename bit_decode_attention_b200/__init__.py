@@ -542,7 +542,8 @@ def nvfp4_kv_commit_path(planes, start_pos: torch.Tensor, path: torch.Tensor, n_
                          stream=None) -> None:
     """Keep the accepted path's cache slots: slot start_pos[b] + path[b][j] moves
     to start_pos[b] + j for j < n_accepted[b], in every plane given (all layers'
-    K and V as a KVPlaneList or a sequence of KVPlane; one launch for 64 planes)."""
+    K and V as a KVPlaneList or a sequence of KVPlane, none of them twice; one launch
+    for 64 planes)."""
     _commit_path("nvfp4_kv_commit_path", KVPlane, planes, start_pos, path, n_accepted, new_lens, status, stream)
 
 

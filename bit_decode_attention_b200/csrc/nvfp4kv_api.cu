@@ -1,6 +1,7 @@
 // nvfp4kv_api.cu -- the extern "C" entry points of libnvfp4kv.so declared in
 // include/nvfp4kv.h: argument validation, workspace layout and launches.
 // Every call is asynchronous on the caller's stream and allocates nothing.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -556,6 +557,40 @@ nvfp4_status run_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H
     return from_cuda(launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// token slots of a plane's memory, over all its KV heads
+int64_t plane_slots(const nvfp4_kv_plane& p) { return (int64_t)p.B * p.H_kv * p.S_max; }
+int64_t plane_slots(const nvfp4_kv_paged_plane& p) { return (int64_t)p.num_pages * p.H_kv * p.page_tokens; }
+
+struct Range {
+    uintptr_t lo, hi;
+};
+
+// Whether two of n ranges share a byte.  No memory is allocated: more than 256 are
+// compared pair by pair.
+template <class F>
+bool any_overlap(int n, F range) {
+    bool rising = true;                               // as the slices of one tensor are
+    for (int i = 1; rising && i < n; ++i) rising = range(i - 1).hi <= range(i).lo;
+    if (rising) return false;
+    constexpr int kMost = 256;
+    if (n > kMost) {
+        for (int i = 1; i < n; ++i) {
+            const Range a = range(i);
+            for (int j = 0; j < i; ++j) {
+                const Range b = range(j);
+                if (a.lo < b.hi && b.lo < a.hi) return true;
+            }
+        }
+        return false;
+    }
+    Range r[kMost];
+    for (int i = 0; i < n; ++i) r[i] = range(i);
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (int i = 1; i < n; ++i)
+        if (r[i - 1].hi > r[i].lo) return true;
+    return false;
+}
+
 template <class Plane>
 nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int32_t* d_start_pos,
                              const int32_t* d_path, const int32_t* d_n_accepted, int32_t* d_new_lens,
@@ -573,6 +608,14 @@ nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int
         if (!cache_pair(&planes[0], &planes[i], c)) return NVFP4_ERR_INVALID_ARG;
         if (c.num_pages < a.num_pages) a.num_pages = c.num_pages;
     }
+    // planes are moved at the same time: none may be given twice
+    auto bytes = [&](const uint8_t* at, const Plane& p, int per_slot) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(at);
+        return Range{lo, lo + (uintptr_t)(plane_slots(p) * per_slot)};
+    };
+    if (any_overlap(n_planes, [&](int i) { return bytes(planes[i].codes, planes[i], c.D / 2); }) ||
+        any_overlap(n_planes, [&](int i) { return bytes(planes[i].scales, planes[i], c.D / 16); }))
+        return NVFP4_ERR_INVALID_ARG;
     if (c.B == 0 || N == 0) return NVFP4_OK;
     a.planes = planes;
     a.codes = [](const void* p, int i) { return static_cast<const Plane*>(p)[i].codes; };

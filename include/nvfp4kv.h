@@ -503,7 +503,8 @@ nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_pro
  * path[b][j] moves to slot start_pos[b] + j for j < n_accepted[b], codes and
  * scale bytes of all KV heads, as bytes.  One launch for up to 64 planes.
  *   planes        host array of n_planes planes (all layers' K and V) that agree
- *                 in B, H_kv, S_max and D (paged: in the block table too)
+ *                 in B, H_kv, S_max and D (paged: in the block table too) and
+ *                 share no memory (a plane that layers share is given once)
  *   N             entries of a path row
  *   d_path        device int32 [B][N], strictly increasing up to n_accepted
  *   d_n_accepted  device int32 [B], 0 .. N

@@ -127,6 +127,31 @@ def test_commit_refusals(lib):
     assert call([plane(B=0)]) == 0
 
 
+def test_commit_refuses_planes_that_share_memory(lib):
+    """A launch moves its planes at the same time: one given twice (layers that share a
+    cache), or a part of another, would be moved by two blocks at once."""
+    def call(planes, pg=False):
+        kind = _native.PagedPlaneStruct if pg else _native.KVPlaneStruct
+        f = lib.nvfp4_kv_commit_path_paged if pg else lib.nvfp4_kv_commit_path
+        # d_new_lens aliasing d_start_pos is refused as well; N = 0 ends the accepted calls early
+        return f((kind * len(planes))(*planes), len(planes), 0, DEV, DEV, DEV, None, None, None)
+    code, scale = 2 * 2 * 256 * 64, 2 * 2 * 256 * 8          # bytes of plane()
+    c0, s0 = 1 << 20, 1 << 30
+    at = lambda i, j: plane(codes=c0 + i * code, scales=s0 + j * scale)
+    far = [at(i, i) for i in range(300)]
+    assert call(far[:2]) == 0 and call(far[::-1]) == 0 and call(far[1:150] + far[:1] + far[200:]) == 0
+    for planes in ([at(0, 0), at(0, 0)], [at(0, 0), at(0, 1)], [at(0, 0), at(1, 0)],
+                   [at(0, 0), plane(codes=c0 + code - 16, scales=s0 + 9 * scale)],
+                   [at(1, 1), plane(codes=c0, scales=s0 + scale + 16)],
+                   far + far[7:8], far[9:10] + far[:20], far[::-1] + [far[150]]):
+        assert call(planes) == INVALID
+    pages = 4 * 2 * 128
+    pool = lambda i, j: paged(codes=c0 + i * pages * 64, scales=s0 + j * pages * 8)
+    assert call([pool(0, 0), pool(1, 1), pool(2, 5)], True) == 0
+    for planes in ([pool(0, 0), pool(0, 1)], [pool(0, 0), pool(3, 1), pool(2, 0)]):
+        assert call(planes, True) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(lib, monkeypatch):
     import bit_decode_attention_b200 as nv
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
