@@ -467,6 +467,13 @@ bool cache_pair(const nvfp4_kv_paged_plane* k, const nvfp4_kv_paged_plane* v, Ca
     return true;
 }
 
+// Whether na and nb 32-bit values share memory (nullptr: none).
+bool overlap32(const void* a, int64_t na, const void* b, int64_t nb) {
+    if (a == nullptr || b == nullptr) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
+}
+
 nvfp4_status run_qk_norm_rope_append(const void* x_q, const void* x_k, const void* x_v, nvfp4_dtype dtype, int n_new,
                                      int H_q, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                                      const void* w_q, const void* w_k, float eps, const float* rope_table,
@@ -478,7 +485,10 @@ nvfp4_status run_qk_norm_rope_append(const void* x_q, const void* x_k, const voi
     if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
     if (n_new < 0 || H_q <= 0 || d_s_tensor_k == nullptr || d_s_tensor_v == nullptr || d_start_pos == nullptr)
         return NVFP4_ERR_INVALID_ARG;
-    if (d_new_lens != nullptr && (d_new_lens == d_start_pos || d_new_lens == d_n_valid)) return NVFP4_ERR_INVALID_ARG;
+    // a block writes its sequence's length while others still read these
+    if (overlap32(d_new_lens, c.B, d_start_pos, c.B) || overlap32(d_new_lens, c.B, d_n_valid, c.B) ||
+        overlap32(d_new_lens, c.B, d_positions, (int64_t)c.B * n_new))
+        return NVFP4_ERR_INVALID_ARG;
     if (!std::isfinite(eps)) return NVFP4_ERR_INVALID_ARG;
     if (rope_table == nullptr ? rope_dims != 0 : (rope_dims <= 0 || rope_dims > c.D || rope_dims % 16 != 0 ||
                                                   rope_positions <= 0 || !aligned16(rope_table)))
@@ -597,7 +607,10 @@ nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int
                              int32_t* d_status, nvfp4_stream_t stream) {
     if (n_planes < 0 || N < 0 || (n_planes > 0 && planes == nullptr)) return NVFP4_ERR_INVALID_ARG;
     if (d_start_pos == nullptr || d_path == nullptr || d_n_accepted == nullptr) return NVFP4_ERR_INVALID_ARG;
-    if (d_new_lens != nullptr && (d_new_lens == d_start_pos || d_new_lens == d_n_accepted))
+    const int64_t B = n_planes > 0 ? planes[0].B : 1;
+    // a block writes its sequence's length while others still read these
+    if (overlap32(d_new_lens, B, d_start_pos, B) || overlap32(d_new_lens, B, d_n_accepted, B) ||
+        overlap32(d_new_lens, B, d_path, B * N))
         return NVFP4_ERR_INVALID_ARG;
     if (N > kTreeMaxNodes) return NVFP4_ERR_UNSUPPORTED;
     if (n_planes == 0) return NVFP4_OK;
@@ -685,6 +698,19 @@ nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_pro
     if (target_probs == nullptr || d_tokens == nullptr || d_parents == nullptr || d_u_accept == nullptr ||
         d_u_sample == nullptr || d_path == nullptr || d_n_accepted == nullptr || d_next_token == nullptr)
         return NVFP4_ERR_INVALID_ARG;
+    // A path is written while other blocks still read the inputs; the other outputs after
+    // a sequence's last pass, when its n_nodes has been read (the accepted counts may
+    // take its place).
+    const int64_t nodes = (int64_t)B * N, np = parents_shared ? N : nodes;
+    const struct { const void* at; int64_t n; } out[3] = {{d_path, nodes}, {d_n_accepted, B}, {d_next_token, B}},
+        in[4] = {{d_tokens, nodes}, {d_parents, np}, {d_u_accept, nodes}, {d_u_sample, B}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap32(out[i].at, out[i].n, in[j].at, in[j].n)) return NVFP4_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap32(out[i].at, out[i].n, out[j].at, out[j].n)) return NVFP4_ERR_INVALID_ARG;
+    }
+    if (overlap32(d_path, nodes, d_n_nodes, B)) return NVFP4_ERR_INVALID_ARG;
     const uintptr_t esz = dtype == NVFP4_IN_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(target_probs) % esz != 0 || reinterpret_cast<uintptr_t>(draft_probs) % esz != 0)
         return NVFP4_ERR_INVALID_ARG;

@@ -406,7 +406,7 @@ nvfp4_status nvfp4_decode_attention_noalloc(const void* q, nvfp4_dtype q_dtype, 
  *   d_start_pos    device int32 [B]: token i goes to slot start_pos[b] + i
  *   d_n_valid      device int32 [B] or NULL: tokens of each sequence
  *   d_new_lens     device int32 [B] or NULL: written with start + n_valid; must
- *                  not alias d_start_pos or d_n_valid
+ *                  not overlap d_start_pos, d_n_valid or d_positions
  *   q_out          device [B][n_new][H_q][D] of `dtype`, 16-byte aligned; must
  *                  not overlap the inputs
  * A sequence with start < 0 or start + n_valid > S_max is skipped entirely
@@ -489,6 +489,8 @@ nvfp4_status nvfp4_tree_attention_paged(const void* q, nvfp4_dtype q_dtype, int 
  *   d_path        device int32 [B][N]: the accepted nodes from node 0 on, then -1
  *   d_n_accepted  device int32 [B]: nodes of the path (>= 1)
  *   d_next_token  device int32 [B]
+ * The outputs must overlap neither the inputs nor each other; d_n_accepted may be
+ * d_n_nodes.
  * NaN and negative probabilities count as 0.  A node with a bad token or
  * parent is never accepted, with NVFP4_ERR_INVALID_ARG.  A last row without a
  * positive finite sum gives token -1 and NVFP4_ERR_NONFINITE.  A sequence of
@@ -509,7 +511,7 @@ nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_pro
  *   d_path        device int32 [B][N], strictly increasing up to n_accepted
  *   d_n_accepted  device int32 [B], 0 .. N
  *   d_new_lens    device int32 [B] or NULL: start_pos + n_accepted; must not
- *                 alias d_start_pos or d_n_accepted
+ *                 overlap d_start_pos, d_path or d_n_accepted
  * A sequence whose path is not increasing, or leaves [0, N), is skipped with
  * NVFP4_ERR_INVALID_ARG; one that passes S_max with NVFP4_ERR_CAPACITY.
  * Paged: a block-table entry outside the pool skips its node with

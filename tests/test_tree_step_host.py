@@ -152,6 +152,40 @@ def test_commit_refuses_planes_that_share_memory(lib):
         assert call(planes, True) == INVALID
 
 
+def test_outputs_over_inputs_are_refused(lib):
+    """Whole numbers that a call writes, over ones that its other blocks may still read."""
+    at = lambda i: ctypes.c_void_p(1 << 20 | 4 * i)
+    for pg in (False, True):
+        # B = 2, n = 3: positions 10 .. 15, starts 20, 21, counts 30, 31
+        a = dict(n=3, P=1 << 20, pos=at(10), start=at(20), valid=at(30), pg=pg)
+        for i in (9, 10, 12, 15, 19, 20, 21, 29, 31):
+            assert norm_rope(lib, lens=at(i), **a) == INVALID, i
+        for i in (8, 16, 18, 22, 28, 32):                    # apart: the next check is reached
+            assert norm_rope(lib, lens=at(i), **dict(a, n=1 << 30, pos=None)) == UNSUP, i
+
+    def commit(lens, pg):
+        one = paged() if pg else plane()
+        f = lib.nvfp4_kv_commit_path_paged if pg else lib.nvfp4_kv_commit_path
+        return f(ctypes.byref(one), 1, 3, at(20), at(10), at(30), at(lens), None, None)
+    for pg in (False, True):
+        for i in (9, 10, 15, 19, 21, 29, 31):
+            assert commit(i, pg) == INVALID, i
+
+    def verify(**kw):
+        b = dict(tok=at(10), par=at(20), sh=0, ua=at(30), us=at(40), nodes=at(50), path=at(100), na=at(110), nx=at(120), N=3)
+        b.update(kw)
+        return lib.nvfp4_verify_drafts(DEV, DEV, 1, 2, b["N"], 100, b["tok"], b["par"], b["sh"], b["ua"], b["us"],
+                                       b["nodes"], b["path"], b["na"], b["nx"], None, None)
+    for i in (5, 10, 15, 16, 20, 25, 30, 35, 39, 41, 46, 50, 51):
+        assert verify(path=at(i)) == INVALID, i
+    for name in ("na", "nx"):
+        for i in (9, 15, 20, 25, 29, 35, 39, 41, 99, 100, 105):
+            assert verify(**{name: at(i)}) == INVALID, (name, i)
+    assert verify(na=at(119)) == INVALID
+    # parents of one tree for all sequences: N of them
+    assert verify(path=at(22), sh=1) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(lib, monkeypatch):
     import bit_decode_attention_b200 as nv
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
