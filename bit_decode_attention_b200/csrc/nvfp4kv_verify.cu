@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
         sm.token[i] = tok;
         sm.ua[i] = ua;
         sm.pp[i] = ok && i < n ? load1<F32>(q.p, (row0 + par) * V + tok) : 0.0f;
-        sm.dd[i] = DRAFT && ok && i < n ? load1<F32>(q.d, (row0 + par) * V + tok) : 1.0f;
+        sm.dd[i] = DRAFT && ok && i < n ? fmaxf(load1<F32>(q.d, (row0 + par) * V + tok), 0.0f) : 1.0f;
     }
     if (n < 1 || n > N) {                             // 0: a padding row, left as it was
         if (n != 0 && rank == 0 && tid == 0) report(q.status, NVFP4_ERR_INVALID_ARG);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
     double Z = 1.0;
     bool sums_valid = false;                          // warp_sum and total hold the current weights' sums
 
-    // E weights at once, of tokens x, x + 1, .. (probability pv, draft dv), after the
+    // E weights at once, of tokens x, x + 1, .. (probability pv, draft dv >= 0), after the
     // first k rejections.  NaN counts as 0.  (The loop over rejections stays rolled:
     // unrolled over elements too, the code would be the kernel's time.)
     auto weights = [&](auto& w, const auto& pv, const auto& dv, int x, int k) {
@@ -187,7 +187,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
                 for (int e = 0; e < VEC; ++e) pv[u][e] = dv[u][e] = 0.0f;
                 if (i < hi) {
                     load_vec<F32, VEC>(q.p, base + i, pv[u]);
-                    if (DRAFT && k > 0) load_vec<F32, VEC>(q.d, base + i, dv[u]);
+                    if (DRAFT && k > 0) {
+                        load_vec<F32, VEC>(q.d, base + i, dv[u]);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) dv[u][e] = fmaxf(dv[u][e], 0.0f);
+                    }
                 }
             }
 #pragma unroll
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
                 float pv[1] = {0.0f}, dv[1] = {0.0f};
                 if (i < s1) {
                     pv[0] = load1<F32>(q.p, base + i);
-                    if (DRAFT && nrej > 0) dv[0] = load1<F32>(q.d, base + i);
+                    if (DRAFT && nrej > 0) dv[0] = fmaxf(load1<F32>(q.d, base + i), 0.0f);
                 }
                 double w[1];
                 weights(w, pv, dv, (int)i, nrej);
