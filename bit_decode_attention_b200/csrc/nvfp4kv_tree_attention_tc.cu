@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
                     const float cs = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.17549435e-38f);
 #pragma unroll
                     for (int j = 0; j < 4 * NP; ++j)
-                        x[j] = pack_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up);
+                        x[j] = amax < 0x7F800000u
+                                   ? pack_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up)
+                                   : 0x7FFF7FFFu;     // an infinity or a NaN in the row: all of its scores are NaN
 #pragma unroll 1
                     for (int c = 0; c < copies; ++c) {
                         const int at = row + c * rows, rb = at >> 7;
@@ -748,7 +750,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
             // (the last two items' P . V: one of each group, or there was one item)
             for (uint32_t x = gi >= 2 ? gi - 2 : 0; x < gi; ++x)
                 wait_warp(&sm.pdone[x & 1], (x >> 1) & 1, abort_flag, p.status, polls);
-            sm.ml[h][0][r] = live ? m_run : -INFINITY;
+            // A NaN among the row's weights (all of its scores, then) is carried in m: the
+            // running maximum passes NaN by, and -infinity says that nothing was seen.
+            sm.ml[h][0][r] = live ? (l_run == l_run ? m_run : l_run) : -INFINITY;
             sm.ml[h][1][r] = live ? l_run : 0.0f;
             softmax_sync();
             tc::fence_after_sync();
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
             for (int i = 0; i < 8; ++i)
                 if (m8[i] != -INFINITY)
                     l_all = __fmaf_rn(sm.ml[i >> 2][1][lr + (i & 3) * rows_per], fast_exp2(m8[i] - m_all), l_all);
-            const float inv = whole ? (l_all > 0.0f ? 1.0f / l_all : 0.0f) : 1.0f;
+            const float inv = whole ? (l_all == 0.0f ? 0.0f : 1.0f / l_all) : 1.0f;
             // factors of the groups' O (of this copy); 0 where a group saw nothing: O is anything then
             float fo[2], ff[2];                       // of O, and of what was flushed of it
             int flushed[2];
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_tc_kernel(const
                 }
             }
             if (!whole && live && part == 0 && (dual || h == 0)) {
-                reinterpret_cast<float2*>(slot + (int64_t)RB * T * D)[row] = make_float2(m_all, l_all);
+                reinterpret_cast<float2*>(slot + (int64_t)RB * T * D)[row] = make_float2(l_all == l_all ? m_all : l_all, l_all);
             }
             tc::fence_before_sync();
             softmax_sync();                           // O, the query buffer and the exchanges have been read
@@ -921,9 +925,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
         M = Mn;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            // a contributor that saw nothing left its O undefined
+            // a contributor that saw nothing left its O undefined; a NaN maximum stays one
             const float w = j0 + k >= parts || ml[k].x == -INFINITY ? 0.0f : fast_exp2(ml[k].x - M);
-            if (w > 0.0f) {
+            if (w != 0.0f) {
                 L = __fmaf_rn(ml[k].y, w, L);
                 acc.x = __fmaf_rn(o[k].x, w, acc.x);
                 acc.y = __fmaf_rn(o[k].y, w, acc.y);
@@ -932,7 +936,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
         }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int nd = (int)p.fd_g.div((uint32_t)(gr0 + row));
     const int64_t at =
         (((int64_t)d.y * p.N + nd) * p.Hq + (int64_t)d.z * p.g + (gr0 + row - nd * p.g)) * D + col;

@@ -455,7 +455,8 @@ size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D);
  *                probabilities enter the second product as two f16 terms (about
  *                22 bits); bf16: as one, whose rounding (2^-11) is below the output's
  *   workspace    >= nvfp4_tree_attention_workspace(...) bytes, 16-byte aligned
- * A node that sees nothing gives a zero row.  A sequence with start_pos < 0 or
+ * A node that sees nothing gives a zero row; else a query row with an infinity or
+ * a NaN gives NaN.  A sequence with start_pos < 0 or
  * start_pos + nodes > S_max is skipped with NVFP4_ERR_CAPACITY (its rows are
  * left as they were).  Paged: as for nvfp4_decode_attention_paged. */
 nvfp4_status nvfp4_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H_q, const nvfp4_kv_plane* k,

@@ -1,10 +1,12 @@
 """The tree-step operators on the GPU at the ends of their documented ranges: nodes and
 group sizes up to the limits, values that are no numbers, rows that nobody computes."""
+import numpy as np
 import pytest
 import torch
 
+import synthetic
 import tree_reference as ref
-from test_gpu_tree_step import dev, make_verify, status
+from test_gpu_tree_step import block_table, dev, i32, make_verify, status, to_pages
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +69,51 @@ def test_verify_rows_strewn_with_entries_that_are_no_probabilities(nv, N, V, kin
                 d[b, par[i], tok[b, i]] = float("nan") if r[b, i] < 0.25 else -0.5
     st, _ = check_cleaned_verify(nv, p, d, tok, par, ua, us)
     assert st == 0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N,g,D,starts,paged", [
+    (4, 4, 128, [60], False), (8, 4, 128, [5000, 1], False), (16, 4, 64, [3000, 130], True), (24, 5, 128, [4000, 9], False),
+    (33, 8, 128, [2500, 0], False), (33, 8, 64, [0, 2500], True)])
+def test_tree_attention_of_a_query_that_is_no_number(nv, N, g, D, starts, paged, bf16):
+    """A query with a NaN or an infinity gives NaN where it sees a token, and nothing to
+    the other rows; a node that sees nothing gives zeros whatever its query holds."""
+    B, Hkv = len(starts), 2
+    S = -(-(max(starts) + N) // 128) * 128
+    c, s = synthetic.random_planes(N, B, Hkv, S, D, max_scale_byte=0x50)
+    t4 = [c, s, c.flip(2).contiguous(), s.flip(2).contiguous()]
+    if paged:
+        tbl = block_table(B, S // 128, 3)
+        t4 = to_pages(t4, tbl, 128)
+        tbl = tbl.cuda()
+    t4 = [t.cuda() for t in t4]
+    mk = (lambda a, b: nv.PagedKVPlane(a, b, tbl)) if paged else nv.KVPlane
+    k, v = mk(t4[0], t4[1]), mk(t4[2], t4[3])
+    call = nv.nvfp4_tree_attention_paged if paged else nv.nvfp4_tree_attention
+    seen = np.stack([ref.ancestors(ref.parents_of("tree", N))] * B)
+    seen[:, N - 1] = False
+    q = torch.randn(B, N, g * Hkv, D, generator=torch.Generator().manual_seed(N)).bfloat16().cuda()
+    sc, mask, st = torch.tensor([0.01], device="cuda"), dev(ref.mask_words(seen)), status()
+
+    def run(q):
+        ws = torch.full((nv.nvfp4_tree_attention_workspace(B, N, g * Hkv, Hkv, D),), 0xFF, dtype=torch.uint8, device="cuda")
+        out = call(q, k, v, sc, sc, i32(starts), tree_mask=mask, out_dtype=torch.bfloat16 if bf16 else torch.float32,
+                   workspace=ws, status=st)
+        assert st.item() == 0
+        return out
+    want, bad = run(q), torch.zeros(B, N, g * Hkv, dtype=torch.bool)
+    assert want.isfinite().all()
+    nan, inf = float("nan"), float("inf")
+    for i, (value, at) in enumerate([(nan, 0), (inf, D - 1), (-inf, 7), (nan, slice(None)), (-inf, slice(None))]):
+        for b in range(B):
+            n, h = (5 * i + b) % N, (3 * i + 1) % (g * Hkv)
+            q[b, n, h, at] = value
+            bad[b, n, h] = True
+    q[:, N - 1, 0, 3] = nan
+    bad[:, N - 1, 0] = True
+    blind = torch.zeros_like(bad)
+    for b in range(B):
+        blind[b, N - 1] = starts[b] == 0
+    got, bad, blind = run(q), bad.cuda(), blind.cuda()
+    assert got[bad & ~blind].isnan().all()
+    assert torch.equal(got[~bad], want[~bad]) and (got[blind] == 0).all()
