@@ -371,17 +371,18 @@ def _allocating(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _like_rows(x: torch.Tensor, counts, dtype, stream) -> torch.Tensor:
-    """A dense output like x; with `counts` the rows behind them are not written: zeros."""
+def _like_rows(x: torch.Tensor, dtype, stream) -> torch.Tensor:
+    """A dense output like x, zeros: rows behind a sequence's count, and rows of a sequence
+    or token that the kernel refuses, are not written."""
     with _allocating(stream):
-        return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=dtype, device=x.device)
+        return torch.zeros(x.shape, dtype=dtype, device=x.device)
 
 
 def _qk_norm_rope_append(func, kind, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps, rope_table,
                          interleaved, positions, n_valid, q_out, new_lens, status, stream):
     _need_kind(k, v, kind)
     if q_out is None:
-        q_out = _like_rows(x_q, n_valid, x_q.dtype, stream)
+        q_out = _like_rows(x_q, x_q.dtype, stream)
     st = _native.binding().qk_norm_rope_append(
         *_target(stream), kind is PagedKVPlane, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v, k, v, w_q, w_k, eps,
         rope_table, interleaved, positions, n_valid, q_out, new_lens, status)
@@ -401,7 +402,8 @@ def nvfp4_qk_norm_rope_append(x_q: torch.Tensor, x_k: torch.Tensor, x_v: torch.T
     """RMS norm of each query and key head (eps < 0: none), rotation by the rows
     of rope_table [P][R] (R/2 cosines, R/2 sines; None: none), K and V quantized
     into the cache at slots start_pos[b] + i; returns the queries [B][n][H_q][D].
-    x_q, x_k, x_v [B][n][heads][D] may be slices of one packed projection."""
+    x_q, x_k, x_v [B][n][heads][D] may be slices of one packed projection.  Rows
+    that are not computed (padding, refused ones) are zero where q_out is None."""
     return _qk_norm_rope_append("nvfp4_qk_norm_rope_append", KVPlane, x_q, x_k, x_v, start_pos, s_tensor_k, s_tensor_v,
                                 k, v, w_q, w_k, eps, rope_table, interleaved, positions, n_valid, q_out, new_lens,
                                 status, stream)
@@ -429,7 +431,7 @@ def _tree_attention(func, kind, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree
                     out_dtype, workspace, status, stream):
     _need_kind(k, v, kind)
     if out is None:
-        out = _like_rows(q, n_nodes, out_dtype, stream)
+        out = _like_rows(q, out_dtype, stream)
     if workspace is None:
         B, N, H_q, D = q.shape
         size = nvfp4_tree_attention_workspace(B, N, H_q, k.codes.shape[1], D)
@@ -454,7 +456,8 @@ def nvfp4_tree_attention(q: torch.Tensor, k: KVPlane, v: KVPlane, s_tensor_k: to
     """Attention of a tree's N nodes (K/V appended at start_pos[b] + i) over the
     cache; q [B][N][H_q][D] bf16 -> [B][N][H_q][D] of out_dtype.  tree_mask int32
     [N][ceil(N/32)] or [B][N][ceil(N/32)]: bit j of row i lets node i see node j
-    (None: a chain, j <= i)."""
+    (None: a chain, j <= i).  Rows that are not computed (padding, refused
+    sequences) are zero where out is None."""
     return _tree_attention("nvfp4_tree_attention", KVPlane, q, k, v, s_tensor_k, s_tensor_v, start_pos, tree_mask,
                            n_nodes, softmax_scale, out, out_dtype, workspace, status, stream)
 

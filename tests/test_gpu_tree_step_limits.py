@@ -6,7 +6,7 @@ import torch
 
 import synthetic
 import tree_reference as ref
-from test_gpu_tree_step import block_table, dev, i32, make_verify, status, to_pages
+from test_gpu_tree_step import block_table, dev, i32, make_rope, make_verify, status, to_pages
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,31 @@ def test_tree_attention_of_a_query_that_is_no_number(nv, N, g, D, starts, paged,
     got, bad, blind = run(q), bad.cuda(), blind.cuda()
     assert got[bad & ~blind].isnan().all()
     assert torch.equal(got[~bad], want[~bad]) and (got[blind] == 0).all()
+
+
+def test_rows_that_are_not_computed_are_zero_in_outputs_a_call_makes(nv):
+    """Refused sequences and tokens, without counts and without an output of the caller's."""
+    q = torch.randn(2, 4, 4, 128, device="cuda").bfloat16()
+    x = torch.randn(2, 4, 1, 128, device="cuda").bfloat16()
+    k, v = (nv.KVPlane.allocate(2, 1, 64, 128) for _ in range(2))
+    sc, tab = torch.tensor([0.01], device="cuda"), make_rope(64, 128).cuda()
+
+    def after_junk(call, dtype=torch.bfloat16):
+        junk = [torch.full((2, 4, 4, 128), float("nan"), dtype=dtype, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        return call()
+    st = status()
+    for dtype in (torch.bfloat16, torch.float32):
+        got = after_junk(lambda: nv.nvfp4_tree_attention(q, k, v, sc, sc, i32([61, 0]), out_dtype=dtype, status=st), dtype)
+        assert st.item() == nv.NVFP4_ERR_CAPACITY and (got == 0).all()          # (the cache holds zeros)
+    st = status()
+    got = after_junk(lambda: nv.nvfp4_qk_norm_rope_append(q, x, x, i32([0, 61]), sc, sc, k, v, rope_table=tab, status=st))
+    assert st.item() == nv.NVFP4_ERR_CAPACITY and (got[1] == 0).all() and (got[0] != 0).any()
+    st = status()
+    got = after_junk(lambda: nv.nvfp4_qk_norm_rope_append(q, x, x, i32([0, 0]), sc, sc, k, v, rope_table=tab, status=st,
+                                                          positions=i32([[0, 1, 64, 2], [0, 1, 2, 3]])))
+    assert st.item() == nv.NVFP4_ERR_INVALID_ARG and (got[0, 2] == 0).all() and (got[0, 3] != 0).any()
+    st = status()
+    got = after_junk(lambda: nv.nvfp4_qk_norm_rope_append(q, x, x, i32([0, 0]), sc * 0, sc, k, v, status=st))
+    assert st.item() == nv.NVFP4_ERR_NONFINITE and (got == 0).all()
