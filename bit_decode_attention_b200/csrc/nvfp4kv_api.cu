@@ -606,7 +606,7 @@ nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int
                              const int32_t* d_path, const int32_t* d_n_accepted, int32_t* d_new_lens,
                              int32_t* d_status, nvfp4_stream_t stream) {
     if (n_planes < 0 || N < 0 || (n_planes > 0 && planes == nullptr)) return NVFP4_ERR_INVALID_ARG;
-    if (d_start_pos == nullptr || d_path == nullptr || d_n_accepted == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (d_start_pos == nullptr || (d_path == nullptr && N > 0) || d_n_accepted == nullptr) return NVFP4_ERR_INVALID_ARG;
     const int64_t B = n_planes > 0 ? planes[0].B : 1;
     // a block writes its sequence's length while others still read these
     if (overlap32(d_new_lens, B, d_start_pos, B) || overlap32(d_new_lens, B, d_n_accepted, B) ||

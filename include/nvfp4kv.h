@@ -413,7 +413,8 @@ nvfp4_status nvfp4_decode_attention_noalloc(const void* q, nvfp4_dtype q_dtype, 
  * with NVFP4_ERR_CAPACITY; a position outside the table skips its token with
  * NVFP4_ERR_INVALID_ARG; a bad tensor scale skips everything with
  * NVFP4_ERR_NONFINITE.  Paged: a block-table entry outside the pool skips the
- * token's K and V with NVFP4_ERR_INVALID_ARG. */
+ * token's K and V with NVFP4_ERR_INVALID_ARG.  n_new == 0 is a no-op (d_new_lens
+ * is left as it was). */
 nvfp4_status nvfp4_qk_norm_rope_append(const void* x_q, const void* x_k, const void* x_v, nvfp4_dtype dtype,
                                        int n_new, int H_q, int64_t q_stride, int64_t k_stride,
                                        int64_t v_stride, const void* w_q, const void* w_k, float eps,
@@ -508,7 +509,7 @@ nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_pro
  *   planes        host array of n_planes planes (all layers' K and V) that agree
  *                 in B, H_kv, S_max and D (paged: in the block table too) and
  *                 share no memory (a plane that layers share is given once)
- *   N             entries of a path row
+ *   N             entries of a path row, at most 1024
  *   d_path        device int32 [B][N], strictly increasing up to n_accepted
  *   d_n_accepted  device int32 [B], 0 .. N
  *   d_new_lens    device int32 [B] or NULL: start_pos + n_accepted; must not
@@ -516,7 +517,8 @@ nvfp4_status nvfp4_verify_drafts(const void* target_probs, const void* draft_pro
  * A sequence whose path is not increasing, or leaves [0, N), is skipped with
  * NVFP4_ERR_INVALID_ARG; one that passes S_max with NVFP4_ERR_CAPACITY.
  * Paged: a block-table entry outside the pool skips its node with
- * NVFP4_ERR_INVALID_ARG. */
+ * NVFP4_ERR_INVALID_ARG.  N == 0 or n_planes == 0 is a no-op (d_path may be NULL,
+ * d_new_lens is left as it was). */
 nvfp4_status nvfp4_kv_commit_path(const nvfp4_kv_plane* planes, int n_planes, int N,
                                   const int32_t* d_start_pos, const int32_t* d_path,
                                   const int32_t* d_n_accepted, int32_t* d_new_lens, int32_t* d_status,

@@ -145,3 +145,16 @@ def test_rows_that_are_not_computed_are_zero_in_outputs_a_call_makes(nv):
     st = status()
     got = after_junk(lambda: nv.nvfp4_qk_norm_rope_append(q, x, x, i32([0, 0]), sc * 0, sc, k, v, status=st))
     assert st.item() == nv.NVFP4_ERR_NONFINITE and (got == 0).all()
+
+
+def test_nothing_to_do_is_no_call(nv):
+    """No tokens, no nodes: nothing is written, new_lens neither."""
+    k, v = (nv.KVPlane.allocate(2, 1, 64, 128) for _ in range(2))
+    q = torch.zeros(2, 0, 4, 128, device="cuda").bfloat16()
+    x = torch.zeros(2, 0, 1, 128, device="cuda").bfloat16()
+    sc, st, lens = torch.tensor([0.01], device="cuda"), status(), i32([-5, -5])
+    assert nv.nvfp4_qk_norm_rope_append(q, x, x, i32([3, 4]), sc, sc, k, v, new_lens=lens, status=st).shape == q.shape
+    assert nv.nvfp4_tree_attention(q, k, v, sc, sc, i32([3, 4]), status=st).shape == q.shape
+    nv.nvfp4_kv_commit_path([k, v], i32([3, 4]), torch.zeros(2, 0, dtype=torch.int32, device="cuda"), i32([0, 0]),
+                            new_lens=lens, status=st)
+    assert lens.tolist() == [-5, -5] and st.item() == 0 and not k.codes.any()

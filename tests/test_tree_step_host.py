@@ -186,6 +186,13 @@ def test_outputs_over_inputs_are_refused(lib):
     assert verify(path=at(22), sh=1) == INVALID
 
 
+def test_commit_of_no_nodes_needs_no_path(lib):
+    for pg, one in ((False, plane()), (True, paged())):
+        f = lib.nvfp4_kv_commit_path_paged if pg else lib.nvfp4_kv_commit_path
+        call = lambda n, N: f(ctypes.byref(one), n, N, DEV, None, DEV, None, None, None)
+        assert call(1, 0) == 0 and call(0, 0) == 0 and call(1, 1) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(lib, monkeypatch):
     import bit_decode_attention_b200 as nv
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
