@@ -6,7 +6,8 @@ import torch
 
 import synthetic
 import tree_reference as ref
-from test_gpu_tree_step import block_table, dev, i32, make_rope, make_verify, status, to_pages
+from test_gpu_tree_step import (block_table, check_verify, dev, i32, make_rope, make_verify, run_append, run_tree,
+                                status, to_pages)
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +159,81 @@ def test_nothing_to_do_is_no_call(nv):
     nv.nvfp4_kv_commit_path([k, v], i32([3, 4]), torch.zeros(2, 0, dtype=torch.int32, device="cuda"), i32([0, 0]),
                             new_lens=lens, status=st)
     assert lens.tolist() == [-5, -5] and st.item() == 0 and not k.codes.any()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,starts,kind,paged", [
+    (1, 1024, 2, 1, 128, [300], "tree", False), (2, 1000, 1, 1, 64, [0, 77], "chain", True),
+    (1, 513, 6, 2, 128, [1], "star", True), (1, 5, 128, 1, 128, [400], "tree", False),
+    (2, 3, 256, 2, 64, [1000, 0], "tree", True), (2, 11, 96, 1, 128, [260, 3000], "tree", False),
+    (1, 1, 128, 1, 128, [700], "chain", False), (1, 1, 127, 1, 64, [129], "chain", False)])
+def test_tree_attention_to_its_limits(nv, B, N, Hq, Hkv, D, starts, kind, paged, bf16):
+    """1,024 nodes; 128 query heads of one KV head."""
+    run_tree(nv, B, N, Hq, Hkv, D, starts, kind, bf16, paged=paged, seed=N + Hq)
+
+
+def test_tree_attention_masks_of_many_nodes(nv):
+    rng = np.random.default_rng(8)
+    m = rng.random((2, 700, 700)) < 0.02
+    m[0, 13] = m[1, 699] = False
+    m[1, 5] = True
+    run_tree(nv, 2, 700, 2, 1, 64, [0, 45], bf16=True, masks=m, counts=[700, 650])
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("N,kind", [(257, "chain"), (1024, "chain"), (1024, "tree"), (300, "star"), (1024, "star")])
+def test_verify_to_its_limit(nv, N, kind, draft):
+    """Paths and rejections of hundreds of nodes."""
+    p, d, tok, par, ua, us = make_verify(3, N, 700, kind, N, sharp=1.0)
+    ua[0] = 0.0                                            # every node that may be: the longest path
+    ua[1] = 1.0 - 2.0 ** -24                               # hardly any: all children of the root
+    st, n_acc = check_verify(nv, p, d if draft else None, tok, par, ua, us, counts=[N, N, N - 1], shared=kind != "tree")
+    assert st == 0 and (kind != "chain" or n_acc[0] == N)
+
+
+@pytest.mark.parametrize("D,Hkv,paged", [(128, 2, False), (64, 1, True), (64, 70, False)])
+def test_commit_of_a_thousand_nodes(nv, D, Hkv, paged):
+    rng = np.random.default_rng(Hkv)
+    B, N, S, L = 5, 1024, 2048, 2
+    codes = torch.from_numpy(rng.integers(0, 256, (L, B, Hkv, S, D // 2), dtype=np.uint8))
+    scales = torch.from_numpy(rng.integers(0, 256, (L, B, Hkv, S, D // 16), dtype=np.uint8))
+    start, n_acc = [0, S - N, 1000, 3, 77], [N, 700, 257, 0, 256]
+    path = np.full((B, N), -1, np.int32)
+    for b in range(B):
+        path[b, :n_acc[b]] = np.sort(rng.choice(N, n_acc[b], replace=False))
+    want_c, want_s = codes.clone(), scales.clone()
+    for b in range(B):
+        src = start[b] + torch.from_numpy(path[b, :n_acc[b]].astype(np.int64))
+        want_c[:, b, :, start[b]:start[b] + n_acc[b]] = codes[:, b][:, :, src]
+        want_s[:, b, :, start[b]:start[b] + n_acc[b]] = scales[:, b][:, :, src]
+    lens, st, table = i32([-1] * B), status(), None
+    if paged:
+        table = block_table(B, S // 128, 3)
+        lay = lambda t: torch.stack([to_pages([x], table, 128)[0] for x in t])
+        codes, scales, want_c, want_s = lay(codes), lay(scales), lay(want_c), lay(want_s)
+        table = table.cuda()
+    c, s = codes.cuda(), scales.cuda()
+    planes = [nv.PagedKVPlane(c[i], s[i], table) if paged else nv.KVPlane(c[i], s[i]) for i in range(L)]
+    call = nv.nvfp4_kv_commit_path_paged if paged else nv.nvfp4_kv_commit_path
+    call(planes, i32(start), dev(path), i32(n_acc), new_lens=lens, status=st)
+    assert torch.equal(c.cpu(), want_c) and torch.equal(s.cpu(), want_s)
+    assert lens.tolist() == [a + n for a, n in zip(start, n_acc)] and st.item() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,n,paged", [(128, 1, 3, False), (96, 1, 70, True), (1, 130, 2, False)])
+def test_norm_rope_append_head_counts(nv, Hq, Hkv, n, paged):
+    run_append(nv, 2, n, Hq, Hkv, 128, 128, "bf16", False, True, True, True, paged, seed=Hq)
+    run_append(nv, 2, n, Hq, Hkv, 64, 32, "f32", True, True, False, False, paged, seed=Hq)
+
+
+def test_tree_attention_over_its_own_queries(nv):
+    """bf16 outputs may take the queries' place: a unit reads its rows before it writes them."""
+    for B, N, Hq, Hkv, D, S in ((1, 4, 8, 2, 128, 60), (3, 40, 12, 4, 64, 3000), (2, 64, 8, 2, 128, 9000)):
+        c, s = synthetic.random_planes(4, B, Hkv, (S + N + 15) // 16 * 16, D, max_scale_byte=0x50)
+        k, v = nv.KVPlane(c.cuda(), s.cuda()), nv.KVPlane(c.flip(2).contiguous().cuda(), s.cuda())
+        q, sc = torch.randn(B, N, Hq, D, device="cuda").bfloat16(), torch.tensor([0.01], device="cuda")
+        want = nv.nvfp4_tree_attention(q, k, v, sc, sc, i32([S] * B), out_dtype=torch.bfloat16)
+        for _ in range(5):
+            x = q.clone()
+            assert nv.nvfp4_tree_attention(x, k, v, sc, sc, i32([S] * B), out=x) is x
+            assert torch.equal(x, want)
