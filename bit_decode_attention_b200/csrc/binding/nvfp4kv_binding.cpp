@@ -371,5 +371,11 @@ PyMODINIT_FUNC PyInit__binding() {
     s_scales = PyUnicode_InternFromString("scales");
     s_block_table = PyUnicode_InternFromString("block_table");
     if (s_codes == nullptr || s_scales == nullptr || s_block_table == nullptr) return nullptr;
-    return PyModule_Create(&module);
+    PyObject* const m = PyModule_Create(&module);
+    // the build looks for this text, to tell a module that was built against another torch
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", NVFP4_BINDING_STAMP) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }
