@@ -549,6 +549,12 @@ nvfp4_status run_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H
     if (workspace == nullptr || !aligned16(workspace) ||
         workspace_bytes < tree_attention_workspace(c.B, N, H_q, c.H_kv, c.D))
         return NVFP4_ERR_WORKSPACE;
+    // A unit writes the rows whose queries it has read, and no others: bf16 outputs may lie
+    // over the queries exactly, any other overlap reaches queries that are still to be read.
+    const int64_t elements = (int64_t)c.B * N * H_q * c.D;
+    if (!(q == out && out_dtype == NVFP4_IN_BF16) &&
+        overlap32(q, elements / 2, out, out_dtype == NVFP4_IN_BF16 ? elements / 2 : elements))
+        return NVFP4_ERR_INVALID_ARG;
     TreeLaunch a{};
     a.q = q;
     a.out_bf16 = out_dtype == NVFP4_IN_BF16;

@@ -452,7 +452,8 @@ size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D);
  *                NULL: a chain, node i sees nodes j <= i
  *   mask_stride  words from one sequence's mask to the next; 0: one tree for all
  *   softmax_scale  0 selects 1 / sqrt(D)
- *   out          device [B][N][H_q][D] of out_dtype, 16-byte aligned.  fp32: the
+ *   out          device [B][N][H_q][D] of out_dtype, 16-byte aligned; bf16 may
+ *                take the place of q, no other overlap with it.  fp32: the
  *                probabilities enter the second product as two f16 terms (about
  *                22 bits); bf16: as one, whose rounding (2^-11) is below the output's
  *   workspace    >= nvfp4_tree_attention_workspace(...) bytes, 16-byte aligned

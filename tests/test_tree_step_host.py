@@ -96,6 +96,16 @@ def test_tree_attention_refusals(lib):
         assert lib.nvfp4_tree_attention_workspace(*shape) == 0
 
 
+def test_tree_attention_outputs_over_queries(lib):
+    at = lambda i: ctypes.c_void_p((1 << 20) + 16 * i)
+    units = 2 * 4 * 4 * 128 * 2 // 16                        # of 16 bytes: bf16 queries of two sequences
+    for odt, span in ((0, units), (1, 2 * units)):
+        for pg in (False, True):
+            for i in (1, units // 2, units - 1, 1 - span):
+                assert tree(lib, pg=pg, q=at(0), out=at(i), odt=odt) == INVALID, (odt, i)
+    assert tree(lib, q=at(0), out=at(0), odt=1) == INVALID
+
+
 def test_verify_refusals(lib):
     def call(p=DEV, d=DEV, dt=1, B=2, N=4, V=100, tok=DEV, par=DEV, sh=1, ua=DEV, us=DEV, path=DEV, na=DEV, nx=DEV):
         return lib.nvfp4_verify_drafts(p, d, dt, B, N, V, tok, par, sh, ua, us, None, path, na, nx, None, None)
