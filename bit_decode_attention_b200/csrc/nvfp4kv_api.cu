@@ -546,6 +546,7 @@ nvfp4_status run_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H
                           (((int64_t)N * (H_q / c.H_kv) + 127) / 128);
     const int64_t tiles = ((int64_t)c.S_max + 127) / 128;
     if (units > (int64_t)INT32_MAX / tiles) return NVFP4_ERR_UNSUPPORTED;
+    if (tiles * 128 > (int64_t)INT32_MAX) return NVFP4_ERR_UNSUPPORTED;   // and their tokens
     if (workspace == nullptr || !aligned16(workspace) ||
         workspace_bytes < tree_attention_workspace(c.B, N, H_q, c.H_kv, c.D))
         return NVFP4_ERR_WORKSPACE;

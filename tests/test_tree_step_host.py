@@ -106,6 +106,16 @@ def test_tree_attention_outputs_over_queries(lib):
     assert tree(lib, q=at(0), out=at(0), odt=1) == INVALID
 
 
+def test_tree_attention_refuses_tiles_past_32_bits(lib):
+    """The last tile of a sequence of more than 2^31 - 128 tokens ends past 31 bits."""
+    most = 2 ** 31 - 128
+    for S, want in ((most, WS), (most + 16, UNSUP), (most + 112, UNSUP)):
+        pl = plane(B=1, H=1, S=S)
+        assert tree(lib, k=pl, v=pl, hq=1, N=1, ws=None) == want
+    pl = paged(T=128, M=most // 128, B=1)
+    assert tree(lib, pg=True, k=pl, v=pl, ws=None, N=1, hq=2) == WS
+
+
 def test_verify_refusals(lib):
     def call(p=DEV, d=DEV, dt=1, B=2, N=4, V=100, tok=DEV, par=DEV, sh=1, ua=DEV, us=DEV, path=DEV, na=DEV, nx=DEV):
         return lib.nvfp4_verify_drafts(p, d, dt, B, N, V, tok, par, sh, ua, us, None, path, na, nx, None, None)
