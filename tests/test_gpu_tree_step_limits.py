@@ -1,5 +1,9 @@
 """The tree-step operators on the GPU at the ends of their documented ranges: nodes and
 group sizes up to the limits, values that are no numbers, rows that nobody computes."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -237,3 +241,76 @@ def test_tree_attention_over_its_own_queries(nv):
             x = q.clone()
             assert nv.nvfp4_tree_attention(x, k, v, sc, sc, i32([S] * B), out=x) is x
             assert torch.equal(x, want)
+
+
+def test_tree_attention_beside_other_calls(nv):
+    """Two streams' tree attention with workspaces of their own, decode attention and
+    verification at the same time."""
+    c, s = synthetic.random_planes(6, 4, 4, 4096, 128, max_scale_byte=0x50)
+    k, v = nv.KVPlane(c.cuda(), s.cuda()), nv.KVPlane(c.flip(2).contiguous().cuda(), s.cuda())
+    sc = torch.tensor([0.01], device="cuda")
+    ver = [dev(t) for t in make_verify(8, 6, 20000, "tree", 3)]
+    jobs = []
+    for N, Hq, start in ((8, 16, 4000), (40, 32, 3000)):
+        q, st = torch.randn(4, N, Hq, 128, device="cuda").bfloat16(), i32([start, 17, start - 99, 0])
+        ws = torch.empty(nv.nvfp4_tree_attention_workspace(4, N, Hq, 4, 128), dtype=torch.uint8, device="cuda")
+        jobs.append(lambda q=q, st=st, ws=ws: nv.nvfp4_tree_attention(q, k, v, sc, sc, st, workspace=ws))
+    qd, lens = torch.randn(4, 16, 128, device="cuda").bfloat16(), i32([4096, 5, 2000, 900])
+    jobs.append(lambda: nv.nvfp4_decode_attention(qd, k, v, sc, sc, lens))
+    jobs.append(lambda: torch.stack([nv.nvfp4_verify_drafts(*ver)[i].flatten()[:8] for i in range(3)]))
+    want = [j() for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(20):
+        for j, st, g in zip(jobs, streams, got):
+            with torch.cuda.stream(st):
+                g.append(j())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, w) for x in g)
+
+
+FIRST_CALL = """
+import torch
+import bit_decode_attention_b200 as nv
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+torch.manual_seed(1)
+k, v = (nv.KVPlane.allocate(1, 2, 256, 128) for _ in range(2))
+x = torch.randn(1, 5, 8, 128, device="cuda").bfloat16()
+kv = torch.randn(1, 5, 2, 128, device="cuda").bfloat16()
+sc, start = torch.tensor([0.004], device="cuda"), i32(100)
+p = torch.softmax(torch.randn(1, 5, 1000, device="cuda"), -1)
+args = p, p.flip(1).contiguous(), i32(*range(5))[None], i32(-1, 0, 0, 1, 1), p[:, :, 0].contiguous(), p[:, 0, 0].contiguous()
+lens = i32(0)
+
+
+def step():
+    q = nv.nvfp4_qk_norm_rope_append(x, kv, kv, start, sc, sc, k, v)
+    o = nv.nvfp4_tree_attention(q, k, v, sc, sc, start)
+    path, n, token = nv.nvfp4_verify_drafts(*args)
+    nv.nvfp4_kv_commit_path([k, v], start, path, n, new_lens=lens)
+    return q, o, path, n, token
+
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (*got, lens, k.codes, v.codes)]
+for t in (k.codes, k.scales, v.codes, v.scales, lens):
+    t.zero_()
+want = (*step(), lens, k.codes, v.codes)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+
+
+def test_a_step_captured_before_any_call(nv):
+    """The process's first calls are captured ones: kernels are loaded and set up then."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=200,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
