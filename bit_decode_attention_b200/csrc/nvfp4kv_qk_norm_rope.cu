@@ -62,7 +62,8 @@ struct NormRopeParams {
 
 // 8 codes (one 32-bit word) and the scale byte of a 16-element block whose
 // other 8 elements the neighbouring lane holds: the arithmetic of
-// quantize_block.  amax, nan: over the whole block.
+// quantize_block, to be kept like it (a test compares the bytes of the two
+// appends).  amax, nan: over the whole block.
 __device__ __forceinline__ uint32_t quantize_half(const float (&v)[8], float amax, bool nan, float st, uint32_t& sb) {
     const float r = __fdiv_rn(amax, __fmul_rn(6.0f, st));
     sb = e4m3_from_float(r);

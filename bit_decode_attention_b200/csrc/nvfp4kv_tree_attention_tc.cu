@@ -22,10 +22,14 @@
 // other's work.  An item is one tile of the unit's rows (alternate tiles go to
 // alternate groups, whose (m, l, O) are merged when the unit ends); a unit of
 // more than 128 rows makes two items of every tile, a row block to each group.
-// Thread r of a group owns row r.  With 64 rows or fewer the rows stand 2 or 4
-// times among the 128, and each copy takes its part of the tile's tokens of the tile's tokens: the softmax's time falls with the rows, at no
-// cost to the MMAs, which multiply 128 rows anyway.  P . V of a copy's tokens writes
-// its lanes of O only (the others are disabled), so that nothing needs zeroing.
+// Thread r of a group owns row r.  With 64 rows or fewer the rows stand 2 or 4 times
+// among the 128, and each copy takes its part of the tile's tokens: the softmax's time
+// falls with the rows, at no cost to the MMAs, which multiply 128 rows anyway.  P . V of
+// a copy's tokens writes its lanes of O only (the others are disabled), so that nothing
+// needs zeroing.
+//
+// A query row with a NaN or an infinity enters as NaN throughout: all of its scores are
+// NaN then, and the row's m and l carry it to the output wherever a token is seen.
 //
 // Warp roles:
 //   warps 0-7    softmax, groups 0 and 1; they also load the queries
@@ -46,13 +50,17 @@
 // Measured (B200, head_dim 128; a tile's raw bytes take 774 clocks of an SM's share
 // of 6.55 TB/s, its MMAs 512 with one row block and 1,024 with two):
 //   128 sequences x 8 KV heads, up to 8 nodes x 4 heads, 1,024 to 8,192 tokens:
-//     358 us, 2,140 clocks a tile.  A loop of waits paces it, for each of two buffers:
-//     dequant 2,300 to 2,900 (the SM issues 0.59 instructions a clock and scheduler,
-//     the integer pipe is 58% busy), then 1,000 of MMA issue and completion.  A
-//     unit's end and the next one's queries take 9,000 clocks beside its tiles.
-//   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 101 us, 4,700 clocks
+//     361 us, 1,870 clocks a tile within a unit.  A loop of waits paces it, for each of two
+//     buffers: dequant 2,300 to 2,900 (the SM issues 0.59 instructions a clock and
+//     scheduler, the integer pipe is 58% busy), then 1,000 of MMA issue and completion.
+//     Between two units of a CTA lie 9,000 to 12,000 clocks: the unit's end, the next
+//     one's queries and first scores.
+//   8 KV heads, 32 nodes x 8 heads (two row blocks), 64K tokens: 101 us, 4,480 clocks
 //     a tile; the softmax paces it: 3,300 of arithmetic (256 x 128 exponentials are
-//     2,048 at the SM's 16 a clock) and 1,400 between P and the next scores
+//     2,048 at the SM's 16 a clock) and 1,200 between P and the next scores
+//   DRAM bytes read are the cache's (172.3 MB for 172.6 with queries and outputs, 32
+//     ragged sequences); the tensor pipe is 42% busy there, 38% at 64K tokens and 51% at
+//     128K with the second term.
 // Tried and slower on the first, each against its day's figure: rows on N, with one
 // exchange of maxima per tile (394 us); 8 dequant warps in place of 16 (451 us, 433);
 // all 16 on each tile (438, 370); e4m3 keys with queries in two e4m3/e5m2 terms and a

@@ -20,7 +20,8 @@
 //
 // Measured (B200): one sequence, 6 nodes over 32,000 tokens: 8.4 us, a chain of
 // memory latencies and cluster barriers.  64 sequences, up to 16 nodes over
-// 131,072: 41 us, where 59 MB of rows take 9 at 6.55 TB/s: a sequence waits for
+// 131,072: 41 to 48 us by the walks, where 59 MB of rows take 9 at 6.55 TB/s (26.7
+// without draft rows, 34.9 with bf16 ones): a sequence waits for
 // two or three passes in turn, of 10 us each; 12 of the 41 are the 64-bit weights
 // (conversions run at 16 a clock and SM).  Loops over elements unrolled further,
 // or the loop over rejections inside them, make the code larger than the
@@ -54,7 +55,7 @@ struct VerifyParams {
     int32_t* next;                                    // [B]
     int32_t* status;
     int64_t parent_stride;
-    int32_t N, V, chunk;                              // chunk: elements of a warp, a multiple of 512
+    int32_t N, V, chunk;                              // chunk: elements of a warp, a multiple of 32 * kWarps
 };
 
 template <bool F32>

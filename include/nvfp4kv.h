@@ -460,7 +460,8 @@ size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D);
  * A node that sees nothing gives a zero row; else a query row with an infinity or
  * a NaN gives NaN.  A sequence with start_pos < 0 or
  * start_pos + nodes > S_max is skipped with NVFP4_ERR_CAPACITY (its rows are
- * left as they were).  Paged: as for nvfp4_decode_attention_paged. */
+ * left as they were).  A bad tensor scale reports NVFP4_ERR_NONFINITE, and the rows
+ * written mean nothing.  Paged: as for nvfp4_decode_attention_paged. */
 nvfp4_status nvfp4_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H_q, const nvfp4_kv_plane* k,
                                   const nvfp4_kv_plane* v, const float* d_s_tensor_k,
                                   const float* d_s_tensor_v, const int32_t* d_start_pos,
