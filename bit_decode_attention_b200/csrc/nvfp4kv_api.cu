@@ -467,6 +467,26 @@ bool cache_pair(const nvfp4_kv_paged_plane* k, const nvfp4_kv_paged_plane* v, Ca
     return true;
 }
 
+// A plane's memory: bytes_per_slot for every token slot of every KV head.
+struct Range {
+    uintptr_t lo, hi;
+};
+int64_t plane_slots(const nvfp4_kv_plane& p) { return (int64_t)p.B * p.H_kv * p.S_max; }
+int64_t plane_slots(const nvfp4_kv_paged_plane& p) { return (int64_t)p.num_pages * p.H_kv * p.page_tokens; }
+template <class Plane>
+Range plane_range(const Plane& p, const uint8_t* at, int bytes_per_slot) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(at);
+    return {lo, lo + (uintptr_t)(plane_slots(p) * bytes_per_slot)};
+}
+bool share(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether two planes (already validated) that a launch writes share memory.
+template <class Plane>
+bool planes_share(const Plane& a, const Plane& b) {
+    return share(plane_range(a, a.codes, a.D / 2), plane_range(b, b.codes, b.D / 2)) ||
+           share(plane_range(a, a.scales, a.D / 16), plane_range(b, b.scales, b.D / 16));
+}
+
 // Whether na and nb 32-bit values share memory (nullptr: none).
 bool overlap32(const void* a, int64_t na, const void* b, int64_t nb) {
     if (a == nullptr || b == nullptr) return false;
@@ -480,8 +500,8 @@ nvfp4_status run_qk_norm_rope_append(const void* x_q, const void* x_k, const voi
                                      int rope_positions, int rope_dims, int rope_interleaved,
                                      const int32_t* d_positions, const int32_t* d_start_pos,
                                      const int32_t* d_n_valid, int32_t* d_new_lens, const float* d_s_tensor_k,
-                                     const float* d_s_tensor_v, const CachePair& c, void* q_out, int32_t* d_status,
-                                     nvfp4_stream_t stream) {
+                                     const float* d_s_tensor_v, const CachePair& c, bool shared, void* q_out,
+                                     int32_t* d_status, nvfp4_stream_t stream) {
     if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
     if (n_new < 0 || H_q <= 0 || d_s_tensor_k == nullptr || d_s_tensor_v == nullptr || d_start_pos == nullptr)
         return NVFP4_ERR_INVALID_ARG;
@@ -508,6 +528,7 @@ nvfp4_status run_qk_norm_rope_append(const void* x_q, const void* x_k, const voi
     // the kernel counts (token, group of four heads) tasks in 31 bits
     if ((int64_t)c.B * n_new > (int64_t)INT32_MAX / ((H_q + 2 * (int64_t)c.H_kv + 3) / 4 + 1))
         return NVFP4_ERR_UNSUPPORTED;
+    if (shared) return NVFP4_ERR_INVALID_ARG;          // K's and V's blocks are written at the same time
     a.xq = x_q; a.xk = x_k; a.xv = x_v;
     a.f32 = dtype == NVFP4_IN_F32;
     a.wq = w_q; a.wk = w_k;
@@ -574,14 +595,6 @@ nvfp4_status run_tree_attention(const void* q, nvfp4_dtype q_dtype, int N, int H
     return from_cuda(launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// token slots of a plane's memory, over all its KV heads
-int64_t plane_slots(const nvfp4_kv_plane& p) { return (int64_t)p.B * p.H_kv * p.S_max; }
-int64_t plane_slots(const nvfp4_kv_paged_plane& p) { return (int64_t)p.num_pages * p.H_kv * p.page_tokens; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-
 // Whether two of n ranges share a byte.  No memory is allocated: more than 256 are
 // compared pair by pair.
 template <class F>
@@ -595,7 +608,7 @@ bool any_overlap(int n, F range) {
             const Range a = range(i);
             for (int j = 0; j < i; ++j) {
                 const Range b = range(j);
-                if (a.lo < b.hi && b.lo < a.hi) return true;
+                if (share(a, b)) return true;
             }
         }
         return false;
@@ -629,12 +642,8 @@ nvfp4_status run_commit_path(const Plane* planes, int n_planes, int N, const int
         if (c.num_pages < a.num_pages) a.num_pages = c.num_pages;
     }
     // planes are moved at the same time: none may be given twice
-    auto bytes = [&](const uint8_t* at, const Plane& p, int per_slot) {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(at);
-        return Range{lo, lo + (uintptr_t)(plane_slots(p) * per_slot)};
-    };
-    if (any_overlap(n_planes, [&](int i) { return bytes(planes[i].codes, planes[i], c.D / 2); }) ||
-        any_overlap(n_planes, [&](int i) { return bytes(planes[i].scales, planes[i], c.D / 16); }))
+    if (any_overlap(n_planes, [&](int i) { return plane_range(planes[i], planes[i].codes, c.D / 2); }) ||
+        any_overlap(n_planes, [&](int i) { return plane_range(planes[i], planes[i].scales, c.D / 16); }))
         return NVFP4_ERR_INVALID_ARG;
     if (c.B == 0 || N == 0) return NVFP4_OK;
     a.planes = planes;
@@ -664,8 +673,8 @@ extern "C" {
         if (!cache_pair(k, v, c)) return NVFP4_ERR_INVALID_ARG;                                                       \
         return run_qk_norm_rope_append(x_q, x_k, x_v, dtype, n_new, H_q, q_stride, k_stride, v_stride, w_q, w_k, eps, \
                                        rope_table, rope_positions, rope_dims, rope_interleaved, d_positions,          \
-                                       d_start_pos, d_n_valid, d_new_lens, d_s_tensor_k, d_s_tensor_v, c, q_out,      \
-                                       d_status, stream);                                                             \
+                                       d_start_pos, d_n_valid, d_new_lens, d_s_tensor_k, d_s_tensor_v, c,             \
+                                       planes_share(*k, *v), q_out, d_status, stream);                                \
     }
 NVFP4_NORM_ROPE_ENTRY(nvfp4_qk_norm_rope_append, nvfp4_kv_plane)
 NVFP4_NORM_ROPE_ENTRY(nvfp4_qk_norm_rope_append_paged, nvfp4_kv_paged_plane)

@@ -409,6 +409,8 @@ nvfp4_status nvfp4_decode_attention_noalloc(const void* q, nvfp4_dtype q_dtype, 
  *                  not overlap d_start_pos, d_n_valid or d_positions
  *   q_out          device [B][n_new][H_q][D] of `dtype`, 16-byte aligned; must
  *                  not overlap the inputs
+ *   k, v           planes that agree in B, H_kv, S_max and D (paged: in the block
+ *                  table too) and share no memory
  * A sequence with start < 0 or start + n_valid > S_max is skipped entirely
  * with NVFP4_ERR_CAPACITY; a position outside the table skips its token with
  * NVFP4_ERR_INVALID_ARG; a bad tensor scale skips everything with

@@ -172,6 +172,17 @@ def test_commit_refuses_planes_that_share_memory(lib):
         assert call(planes, True) == INVALID
 
 
+def test_append_refuses_planes_that_share_memory(lib):
+    c, s = 2 * 2 * 256 * 64, 2 * 2 * 256 * 8                 # bytes of plane()
+    k = plane(codes=1 << 20, scales=1 << 30)
+    for codes, scales in ((1 << 20, 1 << 29), (1 << 25, 1 << 30), ((1 << 20) + c - 16, 1 << 29), (1 << 25, (1 << 30) - s + 16)):
+        assert norm_rope(lib, k=k, v=plane(codes=codes, scales=scales)) == INVALID
+        assert norm_rope(lib, k=plane(codes=codes, scales=scales), v=k) == INVALID
+    k = paged(codes=1 << 20, scales=1 << 30)
+    assert norm_rope(lib, pg=True, k=k, v=paged(codes=1 << 20, scales=1 << 29)) == INVALID
+    assert norm_rope(lib, pg=True, k=k, v=paged(codes=1 << 25, scales=(1 << 30) + 4 * 2 * 128 * 8 - 16)) == INVALID
+
+
 def test_outputs_over_inputs_are_refused(lib):
     """Whole numbers that a call writes, over ones that its other blocks may still read."""
     at = lambda i: ctypes.c_void_p(1 << 20 | 4 * i)
