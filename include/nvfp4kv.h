@@ -457,7 +457,9 @@ size_t nvfp4_tree_attention_workspace(int B, int N, int H_q, int H_kv, int D);
  *   out          device [B][N][H_q][D] of out_dtype, 16-byte aligned; bf16 may
  *                take the place of q, no other overlap with it.  fp32: the
  *                probabilities enter the second product as two f16 terms (about
- *                22 bits); bf16: as one, whose rounding (2^-11) is below the output's
+ *                22 bits); bf16: as one, off by up to 2^-11 of a weight, hence
+ *                of sum p |v| in an output: below the output's own rounding
+ *                except where the sum nearly cancels
  *   workspace    >= nvfp4_tree_attention_workspace(...) bytes, 16-byte aligned
  * A node that sees nothing gives a zero row; else a query row with an infinity or
  * a NaN gives NaN.  A sequence with start_pos < 0 or
